@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
-from typing import Dict, Optional
+from typing import Dict, Optional, Sequence
 
 import torch
 
@@ -24,6 +24,7 @@ FMT_MX_SLAB_A, FMT_MX_SLAB_B = 0x40, 0x80   # OR'ed into FMT_MXFP8: that operand
 FMT_MX_SLAB = FMT_MX_SLAB_A | FMT_MX_SLAB_B
 GROUP_M, GROUP_K = 1, 2
 OUT_BF16, OUT_F32 = 0, 1
+ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2   # BSQ_ACT_*
 NVFP4_QUANTIZE_WORKSPACE_BYTES = 8192   # BSQ_NVFP4_QUANTIZE_WORKSPACE_BYTES
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -68,7 +69,13 @@ def lib():
         L.nvfp4_linear_saved_bytes.restype = C.c_int64
         L.nvfp4_linear_forward.argtypes = [vp, vp, i64, i64, i64, u64, vp, vp, vp, vp, vp]
         L.nvfp4_linear_backward.argtypes = [vp, vp, vp, i64, i64, i64, u64, vp, vp, vp, vp, vp]
-        for f in ("nvfp4_linear_forward", "nvfp4_linear_backward", "nvfp4_quantize", "nvfp4_quantize_noalloc",
+        L.nvfp4_matvec.argtypes = [i32, i64, i64, i64, vp, i64, vp, vp, vp, vp, i32, vp]
+        L.nvfp4_gated_matvec.argtypes = [i32, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.grad_workspace_bytes.argtypes = [i64]
+        L.grad_workspace_bytes.restype = C.c_int64
+        L.grad_sumsq.argtypes = [vp, vp, vp, i64, vp, vp, vp]
+        L.grad_clip.argtypes = [vp, vp, vp, vp, i64, vp, C.c_double, vp, vp]
+        for f in ("nvfp4_matvec", "nvfp4_gated_matvec", "grad_sumsq", "grad_clip", "nvfp4_linear_forward", "nvfp4_linear_backward", "nvfp4_quantize", "nvfp4_quantize_noalloc",
                   "nvfp4_col_mxfp8_row_quantize", "nvfp4_quantize_fprop_wgrad", "nvfp4_quantize_rowscaled",
                   "nvfp4_dequantize", "mxfp8_quantize", "mxfp8_requantize_nvfp4", "rht_apply",
                   "blockscaled_gemm", "blockscaled_grouped_gemm", "bsq_version"):
@@ -407,3 +414,155 @@ def nvfp4_linear_backward(dy: torch.Tensor, w: torch.Tensor, saved: torch.Tensor
         dy.data_ptr(), w.data_ptr(), saved.data_ptr(), T, K, N, sr_seed & (2 ** 64 - 1), sg.data_ptr(),
         workspace.data_ptr(), dx.data_ptr(), dw.data_ptr(), _stream(dev)))
     return dx, dw
+
+
+# ---------------------------------------------------------------- a few tokens on NVFP4 weights
+
+def _tokens(x: torch.Tensor):
+    """x [M, K] bf16 on the device, its elements of a token adjacent; returns (M, K, elements between tokens)."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError("x must be a CUDA/HIP tensor")
+    if x.dtype != torch.bfloat16:
+        raise TypeError("x must have dtype torch.bfloat16, got %s" % x.dtype)
+    if x.dim() != 2:
+        raise ValueError("x must be [tokens, K]")
+    M, K = x.shape
+    if K > 1 and x.stride(1) != 1:
+        raise ValueError("x must have adjacent elements along K")
+    return M, K, x.stride(0) if M > 1 else -(-K // 8) * 8
+
+
+def _weights(codes: torch.Tensor, scales: torch.Tensor, s_enc: torch.Tensor, K: int, name: str, dev):
+    """An NVFP4 weight's checks against K; returns (rows, whether its scale is per row)."""
+    _dev_tensor(codes, torch.uint8, name + "_codes")
+    _dev_tensor(scales, torch.uint8, name + "_scales")
+    _dev_tensor(s_enc, torch.float32, name + "_s_enc")
+    N = codes.shape[0]
+    if codes.dim() != 2 or codes.shape[1] * 2 != K:
+        raise ValueError("%s_codes must be [rows, K/2] with K = %d, got %s" % (name, K, tuple(codes.shape)))
+    if tuple(scales.shape) != (N, K // 16):
+        raise ValueError("%s_scales must be [rows, K/16], got %s" % (name, tuple(scales.shape)))
+    n = s_enc.numel()
+    if n != 1 and n != N:
+        raise ValueError("%s_s_enc must hold 1 value or one per row, got %d" % (name, n))
+    if codes.device != dev or scales.device != dev or s_enc.device != dev:
+        raise ValueError("%s and x must be on one device" % name)
+    return N, n != 1
+
+
+def nvfp4_matvec(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, w_s_enc: torch.Tensor,
+                 out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x [M, K] (bf16, a few tokens; tokens may be strided) times NVFP4 weights [N, K] transposed: y [M, N] in
+    ``out_dtype`` (bf16 or float32).  ``w_s_enc`` holds the weight's tensor scale, or one per row."""
+    M, K, ldx = _tokens(x)
+    dev = x.device
+    N, rows = _weights(w_codes, w_scales, w_s_enc, K, "w", dev)
+    y_dtype = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}[out_dtype]
+    out = _output(out, (M, N), out_dtype, dev)
+    _check("nvfp4_matvec", lib().nvfp4_matvec(
+        FMT_B_ROWSCALED if rows else 0, M, N, K, x.data_ptr(), ldx, w_codes.data_ptr(), w_scales.data_ptr(),
+        w_s_enc.data_ptr(), out.data_ptr(), y_dtype, _stream(dev)))
+    return out
+
+
+def nvfp4_gated_matvec(act: int, x: torch.Tensor, gate_codes: torch.Tensor, gate_scales: torch.Tensor,
+                       gate_s_enc: torch.Tensor, up_codes: torch.Tensor, up_scales: torch.Tensor,
+                       up_s_enc: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """act(x Wg^T) * (x Wu^T) for a few bf16 tokens x [M, K] and NVFP4 weights [F, K], in one kernel: h [M, F]
+    bf16.  ``act`` is ACT_SILU, ACT_GELU or ACT_GELU_TANH; both s_enc hold one tensor scale, or one per row."""
+    M, K, ldx = _tokens(x)
+    dev = x.device
+    F, rows = _weights(gate_codes, gate_scales, gate_s_enc, K, "gate", dev)
+    Fu, urows = _weights(up_codes, up_scales, up_s_enc, K, "up", dev)
+    if Fu != F or urows != rows:
+        raise ValueError("gate and up must agree in rows and in the kind of their tensor scales")
+    out = _output(out, (M, F), torch.bfloat16, dev)
+    _check("nvfp4_gated_matvec", lib().nvfp4_gated_matvec(
+        FMT_B_ROWSCALED if rows else 0, act, M, F, K, x.data_ptr(), ldx, gate_codes.data_ptr(),
+        gate_scales.data_ptr(), gate_s_enc.data_ptr(), up_codes.data_ptr(), up_scales.data_ptr(),
+        up_s_enc.data_ptr(), out.data_ptr(), _stream(dev)))
+    return out
+
+
+def _output(out: Optional[torch.Tensor], shape, dtype, dev) -> torch.Tensor:
+    """The caller's output tensor (checked), or a new one."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _dev_tensor(out, dtype, "out")
+    if tuple(out.shape) != shape:
+        raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), shape))
+    if out.device != dev:
+        raise ValueError("out must be on %s" % (dev,))
+    return out
+
+
+# ---------------------------------------------------------------- gradient clipping
+
+_GRAD_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+class _GradList:
+    """A list of gradients (and outputs) as the C ABI's host arrays."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None):
+        grads = list(grads)
+        if not grads:
+            raise ValueError("the list of gradients is empty")
+        n = len(grads)
+        dev = grads[0].device
+        for i, t in enumerate(grads):
+            if not t.is_cuda or t.device != dev:
+                raise ValueError("gradient %d must be on %s, a GPU" % (i, dev))
+            if t.dtype not in _GRAD_DTYPES:
+                raise TypeError("gradient %d must be bfloat16 or float32, got %s" % (i, t.dtype))
+            if not t.is_contiguous():
+                raise ValueError("gradient %d must be contiguous" % i)
+        self.outs = None
+        if out is not None:
+            out = list(out)
+            if len(out) != n:
+                raise ValueError("out has %d tensors for %d gradients" % (len(out), n))
+            for i, (t, o) in enumerate(zip(grads, out)):
+                if o.dtype != t.dtype or o.shape != t.shape or o.device != dev or not o.is_contiguous():
+                    raise ValueError("out[%d] must be a contiguous tensor like its gradient" % i)
+            self.outs = (C.c_void_p * n)(*[t.data_ptr() for t in out])
+        self.n, self.device = n, dev
+        self.ptrs = (C.c_void_p * n)(*[t.data_ptr() for t in grads])
+        self.numels = (C.c_int64 * n)(*[t.numel() for t in grads])
+        self.dtypes = (C.c_int * n)(*[_GRAD_DTYPES[t.dtype] for t in grads])
+
+    def sumsq(self, workspace: Optional[torch.Tensor]) -> torch.Tensor:
+        s = torch.empty(1, dtype=torch.float64, device=self.device)
+        ws = _workspace(workspace, lib().grad_workspace_bytes(self.n), self.device)
+        _check("grad_sumsq", lib().grad_sumsq(self.ptrs, self.numels, self.dtypes, self.n, s.data_ptr(),
+                                              ws.data_ptr(), _stream(self.device)))
+        return s
+
+    def clip(self, sumsq: torch.Tensor, max_norm: float) -> torch.Tensor:
+        _dev_tensor(sumsq, torch.float64, "sumsq")
+        norm = torch.empty(1, dtype=torch.float32, device=self.device)
+        _check("grad_clip", lib().grad_clip(self.ptrs, self.outs, self.numels, self.dtypes, self.n, sumsq.data_ptr(),
+                                            float(max_norm), norm.data_ptr(), _stream(self.device)))
+        return norm
+
+
+def grad_sumsq(grads: Sequence[torch.Tensor], workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The sum of squares over all gradients (bf16 and float32 tensors) as a float64[1] device tensor; ranks
+    that hold different gradients add theirs up before ``grad_clip``."""
+    return _GradList(grads).sumsq(workspace)
+
+
+def grad_clip(grads: Sequence[torch.Tensor], sumsq: torch.Tensor, max_norm: float,
+              out: Optional[Sequence[torch.Tensor]] = None) -> torch.Tensor:
+    """Scales the gradients by min(1, max_norm / (sqrt(sumsq) + 1e-6)), in place or into ``out``; returns the
+    norm as a float32[1] device tensor."""
+    return _GradList(grads, out).clip(sumsq, max_norm)
+
+
+def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None,
+                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradients' global 2-norm (float32[1], on the device), and the gradients scaled so that it does not
+    exceed ``max_norm``, in place or into ``out``.  ``workspace``: at least grad_workspace_bytes(len(grads))
+    bytes of scratch; one is allocated when none is given."""
+    g = _GradList(grads, out)
+    return g.clip(g.sumsq(workspace), max_norm)

@@ -1,0 +1,81 @@
+// activation.hpp -- the gate activations of a gated feed-forward block, act(g), and their derivatives,
+// in binary32 on the device.
+//
+//   silu       act(g) = g s(g),         s(z) = 1 / (1 + e^-z)
+//   gelu       act(g) = g P(g),         P(g) = erfc(-g / sqrt 2) / 2
+//   gelu_tanh  act(g) = g s(z(g)),      z(g) = sqrt(8/pi) (g + 0.044715 g^3)
+//
+// (0.5 (1 + tanh y) = s(2 y), so the last is the usual tanh form.)  Each is written so that no two
+// nearly equal values are subtracted: the results keep their relative accuracy where act(g) is tiny
+// (g far below zero), and 1 - s is taken as s(-z).
+#pragma once
+
+#include "device_common.hpp"
+
+namespace bsq {
+
+// act and d act / d g.
+struct ActGrad {
+    float f, df;
+};
+
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
+// s(z) and s(-z); e^-z overflowing gives 0 and, through e^-z / (1 + e^-z), would give NaN for s(-z), so
+// the exponential is always taken of -|z|.
+__device__ __forceinline__ void sigmoids(float z, float& s, float& sn) {
+    const float e = exp_fast(-__builtin_fabsf(z));
+    const float r = __builtin_amdgcn_rcpf(1.0f + e);
+    const float small = e * r;
+    s = z >= 0.0f ? r : small;
+    sn = z >= 0.0f ? small : r;
+    if (z != z) s = sn = z;
+}
+
+// P(g) = erfc(-g / sqrt 2) / 2, the normal distribution function.  With x = |g| / sqrt 2 and t = 1 / (1 +
+// x / 2), erfc(x) = t e^(-x^2) Q(t) for a smooth positive Q on (0, 1]; Q's polynomial is a Chebyshev fit
+// made for this file over t in [0.17, 1] (x <= 9.7, below which e^(-x^2) leaves binary32's range); its
+// relative error in binary32 is 2.1e-7.
+__device__ __forceinline__ float normal_cdf(float g) {
+    const float x = __builtin_fabsf(g) * 0.707106781f;
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, x, 1.0f));
+    float q = -0.060039805f;
+    q = __builtin_fmaf(q, t, 0.289117624f);
+    q = __builtin_fmaf(q, t, -0.496166757f);
+    q = __builtin_fmaf(q, t, 0.287778320f);
+    q = __builtin_fmaf(q, t, -0.032907345f);
+    q = __builtin_fmaf(q, t, 0.205159566f);
+    q = __builtin_fmaf(q, t, 0.242528244f);
+    q = __builtin_fmaf(q, t, 0.282447393f);
+    q = __builtin_fmaf(q, t, 0.282082710f);
+    const float half = 0.5f * t * q * exp_fast(-x * x);   // erfc(x) / 2
+    return g >= 0.0f ? 1.0f - half : (g < 0.0f ? half : g);
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float g) {
+    if constexpr (ACT == 1) return g * normal_cdf(g);
+    float z = g;
+    if constexpr (ACT == 2) z = 1.59576912f * __builtin_fmaf(0.044715f * g * g, g, g);
+    // e^-z may overflow to infinity (s = 0) or underflow (s = 1); a NaN passes through
+    return g * __builtin_amdgcn_rcpf(1.0f + exp_fast(-z));
+}
+
+template <int ACT>
+__device__ __forceinline__ ActGrad act_grad(float g) {
+    if constexpr (ACT == 1) {
+        const float p = normal_cdf(g);
+        return {g * p, __builtin_fmaf(g * 0.39894228f, exp_fast(-0.5f * g * g), p)};
+    }
+    float z = g, dz = 1.0f;
+    if constexpr (ACT == 2) {
+        z = 1.59576912f * __builtin_fmaf(0.044715f * g * g, g, g);
+        // kept finite, so that it stays without effect where s(z) s(-z) is 0
+        dz = __builtin_fminf(1.59576912f * __builtin_fmaf(0.134145f * g, g, 1.0f), 3.0e38f);
+    }
+    float s, sn;
+    sigmoids(z, s, sn);
+    return {g * s, __builtin_fmaf(g * s * sn, dz, s)};
+}
+
+}  // namespace bsq

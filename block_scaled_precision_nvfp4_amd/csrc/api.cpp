@@ -453,3 +453,122 @@ int nvfp4_linear_backward(const void* dy, const void* w, const void* saved, int6
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- a few tokens on NVFP4 weights
+
+namespace {
+
+// Checks shared by nvfp4_matvec and nvfp4_gated_matvec (called once for each of its weights).
+int matvec_check(const char* fn, int flags, int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx,
+                 const uint8_t* codes, const uint8_t* scales, const float* s_enc, const void* y) {
+    if (flags & ~BSQ_FMT_B_ROWSCALED)
+        return fail(BSQ_ERR_ARG, "%s: flags must be 0 or BSQ_FMT_B_ROWSCALED, got %d", fn, flags);
+    if (M < 0 || N < 0 || K < 0) return fail(BSQ_ERR_SHAPE, "%s: negative size", fn);
+    if (K % 16 != 0) return fail(BSQ_ERR_SHAPE, "%s: K (%lld) must be a multiple of 16", fn, (long long)K);
+    if (K >= gemm_k_limit(BSQ_FMT_NVFP4))
+        return fail(BSQ_ERR_SHAPE, "%s: K (%lld) exceeds %lld", fn, (long long)K, (long long)gemm_k_limit(BSQ_FMT_NVFP4) - 1);
+    if (M > (int64_t)1 << 20) return fail(BSQ_ERR_SHAPE, "%s: %lld tokens exceed 2^20", fn, (long long)M);
+    if (N > (int64_t)1 << 31) return fail(BSQ_ERR_SHAPE, "%s: %lld weight rows exceed 2^31", fn, (long long)N);
+    if (M == 0 || N == 0) return BSQ_OK;
+    if (!y) return fail(BSQ_ERR_NULL, "%s: the output is NULL", fn);
+    if (!s_enc) return fail(BSQ_ERR_NULL, "%s: NVFP4 needs its tensor scale", fn);
+    if (K > 0 && (!x || !codes || !scales)) return fail(BSQ_ERR_NULL, "%s: operand pointer is NULL", fn);
+    if (K > 0 && (ldx < K || ldx % 8 != 0))
+        return fail(BSQ_ERR_SHAPE, "%s: ldx (%lld) must be a multiple of 8 and at least K", fn, (long long)ldx);
+    if (misaligned(x) || misaligned(codes) || misaligned(scales) || misaligned(y))
+        return fail(BSQ_ERR_ALIGN, "%s: device pointers must be 16-byte aligned", fn);
+    return BSQ_OK;
+}
+
+bool bad_act(int act) { return act != BSQ_ACT_SILU && act != BSQ_ACT_GELU && act != BSQ_ACT_GELU_TANH; }
+
+}  // namespace
+
+extern "C" {
+
+int nvfp4_matvec(int flags, int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const uint8_t* w_codes,
+                 const uint8_t* w_scales, const float* w_s_enc, void* y, int y_dtype, void* hip_stream) {
+    static const char* fn = "nvfp4_matvec";
+    if (y_dtype != BSQ_OUT_BF16 && y_dtype != BSQ_OUT_F32)
+        return fail(BSQ_ERR_ARG, "%s: y_dtype must be 0 (bf16) or 1 (f32), got %d", fn, y_dtype);
+    const int st = matvec_check(fn, flags, M, N, K, x, ldx, w_codes, w_scales, w_s_enc, y);
+    if (st) return st;
+    return launched(bsq::launch_nvfp4_matvec(-1, x, ldx, M, N, K, w_codes, w_scales, w_s_enc, nullptr, nullptr, nullptr,
+                                             flags != 0, y, y_dtype == BSQ_OUT_F32, hip_stream), fn);
+}
+
+int nvfp4_gated_matvec(int flags, int act, int64_t M, int64_t F, int64_t K, const void* x, int64_t ldx,
+                       const uint8_t* gate_codes, const uint8_t* gate_scales, const float* gate_s_enc,
+                       const uint8_t* up_codes, const uint8_t* up_scales, const float* up_s_enc, void* h,
+                       void* hip_stream) {
+    static const char* fn = "nvfp4_gated_matvec";
+    if (bad_act(act)) return fail(BSQ_ERR_ARG, "%s: act must be a BSQ_ACT_* value, got %d", fn, act);
+    int st = matvec_check(fn, flags, M, F, K, x, ldx, gate_codes, gate_scales, gate_s_enc, h);
+    if (st) return st;
+    st = matvec_check(fn, flags, M, F, K, x, ldx, up_codes, up_scales, up_s_enc, h);
+    if (st) return st;
+    return launched(bsq::launch_nvfp4_matvec(act, x, ldx, M, F, K, gate_codes, gate_scales, gate_s_enc, up_codes,
+                                             up_scales, up_s_enc, flags != 0, h, 0, hip_stream), fn);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- gradient clipping
+
+namespace {
+
+int grads_check(const char* fn, const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes,
+                int64_t count) {
+    if (count < 0 || count > (int64_t)1 << 24) return fail(BSQ_ERR_SHAPE, "%s: count (%lld) must be in [0, 2^24]", fn, (long long)count);
+    if (count > 0 && (!grads || !numels || !dtypes)) return fail(BSQ_ERR_NULL, "%s: an array is NULL", fn);
+    int64_t total = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (numels[i] < 0) return fail(BSQ_ERR_SHAPE, "%s: tensor %lld has a negative size", fn, (long long)i);
+        if (numels[i] > ((int64_t)1 << 40) - total) return fail(BSQ_ERR_SHAPE, "%s: more than 2^40 elements", fn);
+        total += numels[i];
+        if (dtypes[i] != BSQ_GRAD_BF16 && dtypes[i] != BSQ_GRAD_F32)
+            return fail(BSQ_ERR_ARG, "%s: tensor %lld: dtype must be 0 (bf16) or 1 (f32), got %d", fn, (long long)i, dtypes[i]);
+        if (numels[i] == 0) continue;
+        const uintptr_t low = dtypes[i] == BSQ_GRAD_F32 ? 3 : 1;
+        if (!grads[i] || (outs && !outs[i])) return fail(BSQ_ERR_NULL, "%s: tensor %lld is NULL", fn, (long long)i);
+        if ((reinterpret_cast<uintptr_t>(grads[i]) & low) || (outs && (reinterpret_cast<uintptr_t>(outs[i]) & low)))
+            return fail(BSQ_ERR_ALIGN, "%s: tensor %lld is not aligned to its elements", fn, (long long)i);
+    }
+    return BSQ_OK;
+}
+
+bool misaligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) != 0; }
+
+}  // namespace
+
+extern "C" {
+
+int64_t grad_workspace_bytes(int64_t count) {
+    if (count < 0 || count > (int64_t)1 << 24) return -1;
+    return bsq::grad_workspace_slots(count) * 8;
+}
+
+int grad_sumsq(const void* const* grads, const int64_t* numels, const int* dtypes, int64_t count, double* sumsq,
+               void* workspace, void* hip_stream) {
+    static const char* fn = "grad_sumsq";
+    const int st = grads_check(fn, grads, nullptr, numels, dtypes, count);
+    if (st) return st;
+    if (!sumsq || !workspace) return fail(BSQ_ERR_NULL, "%s: sumsq or workspace is NULL", fn);
+    if (misaligned8(sumsq) || misaligned(workspace)) return fail(BSQ_ERR_ALIGN, "%s: sumsq or workspace is not aligned", fn);
+    return launched(bsq::launch_grad_sumsq(grads, numels, dtypes, count, sumsq, static_cast<double*>(workspace),
+                                           hip_stream), fn);
+}
+
+int grad_clip(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes, int64_t count,
+              const double* sumsq, double max_norm, float* norm, void* hip_stream) {
+    static const char* fn = "grad_clip";
+    if (!(max_norm >= 0.0)) return fail(BSQ_ERR_ARG, "%s: max_norm must not be negative or NaN", fn);
+    const int st = grads_check(fn, grads, outs, numels, dtypes, count);
+    if (st) return st;
+    if (!sumsq || !norm) return fail(BSQ_ERR_NULL, "%s: sumsq or norm is NULL", fn);
+    if (misaligned8(sumsq) || (reinterpret_cast<uintptr_t>(norm) & 3u))
+        return fail(BSQ_ERR_ALIGN, "%s: sumsq or norm is not aligned", fn);
+    return launched(bsq::launch_grad_clip(grads, outs, numels, dtypes, count, sumsq, max_norm, norm, hip_stream), fn);
+}
+
+}  // extern "C"

@@ -44,6 +44,16 @@ int launch_blockscaled_grouped_gemm(int fmt, int mode, int64_t groups, const int
 int launch_nvfp4_quantize_rowscaled(const void* x, int64_t R, int64_t C, int rounding, uint64_t seed,
                                     uint32_t stream, const int8_t* signs, uint8_t* codes, uint8_t* scales,
                                     float* amax_rows, float* s_enc_rows, void* hip_stream);
+// act < 0: the plain product with the first operand; otherwise the gated pair (BSQ_ACT_*).
+int launch_nvfp4_matvec(int act, const void* x, int64_t ldx, int64_t M, int64_t N, int64_t K, const uint8_t* w_codes,
+                        const uint8_t* w_scales, const float* w_s_enc, const uint8_t* up_codes,
+                        const uint8_t* up_scales, const float* up_s_enc, int rows, void* y, int y_f32,
+                        void* hip_stream);
+int64_t grad_workspace_slots(int64_t count);   // doubles
+int launch_grad_sumsq(const void* const* grads, const int64_t* numels, const int* dtypes, int64_t count,
+                      double* sumsq, double* workspace, void* hip_stream);
+int launch_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes,
+                     int64_t count, const double* sumsq, double max_norm, float* norm, void* hip_stream);
 const char* hip_error_string(int e);
 
 }  // namespace bsq

@@ -411,6 +411,67 @@ int nvfp4_linear_backward(const void* dy, const void* w, const void* saved, int6
                           const int8_t* rht_signs, void* workspace, void* dx, float* dw,
                           void* hip_stream);
 
+/* activations of a gated feed-forward block */
+#define BSQ_ACT_SILU 0        /* g / (1 + e^-g)                                             */
+#define BSQ_ACT_GELU 1        /* g erfc(-g / sqrt 2) / 2                                    */
+#define BSQ_ACT_GELU_TANH 2   /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2            */
+
+/*
+ * nvfp4_matvec -- y[M][N] = x[M][K] W[N][K]^T for a few tokens x in bf16 and NVFP4 weights: the
+ * linear layer of a model that serves single tokens from its quantized weights.  The
+ * activations are not quantized; every weight code * scale enters exactly, products are
+ * summed in fp32 and divided by S once.
+ *   flags   0, or BSQ_FMT_B_ROWSCALED: w_s_enc is float[N] (nvfp4_quantize_rowscaled), else float[1].
+ *   x       bf16, row m at x + m * ldx elements; ldx >= K, ldx % 8 == 0.
+ *   w_codes [N][K/2], w_scales [N][K/16]: rowwise NVFP4 as nvfp4_quantize writes it.  K % 16 == 0.
+ *   y       [M][N], y_dtype BSQ_OUT_BF16 (RNE) or BSQ_OUT_F32.
+ *   M in [0, 2^20], N >= 0, K >= 0 below 2^24; M or N 0 writes nothing, K 0 writes zeros.  Any M is computed;
+ *   from some 64 tokens on, quantizing them and calling blockscaled_gemm is faster.
+ * A NaN or an infinity in a token reaches that token's outputs only, one in a row's scales that
+ * output column only.  The result does not depend on the order in which the GPU runs the work.
+ */
+int nvfp4_matvec(int flags, int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx,
+                 const uint8_t* w_codes, const uint8_t* w_scales, const float* w_s_enc, void* y,
+                 int y_dtype, void* hip_stream);
+
+/*
+ * nvfp4_gated_matvec -- h[M][F] = act(x Wg^T) * (x Wu^T) for a few tokens: both projections, the
+ * activation and the product of a gated feed-forward block in one kernel.  Each projection is
+ * computed as by nvfp4_matvec and kept in fp32 up to the one rounding of h to bf16 (RNE).
+ *   act     BSQ_ACT_*.  gate and up: rowwise NVFP4 [F][K]; flags BSQ_FMT_B_ROWSCALED: both
+ *           s_enc are float[F], else float[1] each.  Otherwise as nvfp4_matvec.
+ */
+int nvfp4_gated_matvec(int flags, int act, int64_t M, int64_t F, int64_t K, const void* x, int64_t ldx,
+                       const uint8_t* gate_codes, const uint8_t* gate_scales, const float* gate_s_enc,
+                       const uint8_t* up_codes, const uint8_t* up_scales, const float* up_s_enc,
+                       void* h, void* hip_stream);
+
+/* gradient element types */
+#define BSQ_GRAD_BF16 0
+#define BSQ_GRAD_F32 1
+
+/*
+ * grad_sumsq / grad_clip -- the global 2-norm of a list of gradients, and the gradients scaled so
+ * that it does not exceed max_norm: N = sqrt(sum of all squares), c = min(1, max_norm / (N +
+ * 1e-6)), out = c * grad rounded once (RNE) to the gradient's type.  Two calls, so that ranks that
+ * hold different gradients can add up their sums in between.
+ *   grads, outs, numels, dtypes  HOST arrays of count entries, read before the call returns:
+ *              device pointers (aligned to their elements; tensors may start anywhere in a flat
+ *              bucket), element counts (0 allowed; at most 2^40 in all), BSQ_GRAD_*.  outs NULL:
+ *              in place.  An out must not overlap another tensor of the list.
+ *   sumsq      double[1] (device): the sum of squares, added in binary64 in a fixed order (the same
+ *              bits on every call); no finite gradient overflows or underflows it.
+ *   workspace  device scratch of grad_workspace_bytes(count) bytes, as for nvfp4_quantize.
+ *   norm       float[1] (device): N.  max_norm >= 0 (infinity: c = 1 for a finite norm).
+ * With c = 1 an in-place call leaves every gradient untouched and an out-of-place one copies it.
+ * A NaN anywhere makes N and every output NaN; an infinite gradient makes N infinite and c 0.
+ */
+int64_t grad_workspace_bytes(int64_t count);
+int grad_sumsq(const void* const* grads, const int64_t* numels, const int* dtypes, int64_t count,
+               double* sumsq, void* workspace, void* hip_stream);
+int grad_clip(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes,
+              int64_t count, const double* sumsq, double max_norm, float* norm, void* hip_stream);
+
 /* Message of the last failing call on this thread ("" if none).  Host memory owned
  * by the library; valid until the thread's next call. */
 const char* bsq_last_error(void);

@@ -1,0 +1,87 @@
+"""Refusals of the feed-forward operators' C entry points, on the host: every invalid argument is
+answered with its documented status before any HIP call."""
+import ctypes as C
+import math
+
+import pytest
+
+FAKE = 0x10000   # 16-byte aligned, never dereferenced
+
+
+@pytest.fixture(scope="module")
+def L():
+    import os
+
+    import block_scaled_precision_nvfp4_amd as bsq
+    if not os.path.exists(bsq.LIB_PATH):
+        from block_scaled_precision_nvfp4_amd import build
+        build.build()
+    return bsq.lib()
+
+
+def mv(L, gated=False, **kw):
+    a = dict(flags=0, act=0, M=2, N=64, K=64, x=FAKE, ldx=64, c=FAKE, s=FAKE, e=FAKE, uc=FAKE, us=FAKE, ue=FAKE, y=FAKE,
+             dt=0)
+    a.update(kw)
+    if gated:
+        return L.nvfp4_gated_matvec(a["flags"], a["act"], a["M"], a["N"], a["K"], a["x"], a["ldx"], a["c"], a["s"],
+                                    a["e"], a["uc"], a["us"], a["ue"], a["y"], None)
+    return L.nvfp4_matvec(a["flags"], a["M"], a["N"], a["K"], a["x"], a["ldx"], a["c"], a["s"], a["e"], a["y"], a["dt"],
+                          None)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("kw,status,needle", [
+    (dict(flags=0x10), 3, "flags"), (dict(M=-1), 2, "negative"), (dict(N=-1), 2, "negative"),
+    (dict(K=-16), 2, "negative"), (dict(K=24), 2, "multiple of 16"), (dict(K=1 << 24, ldx=1 << 24), 2, "exceeds"),
+    (dict(M=(1 << 20) + 1), 2, "tokens"), (dict(N=(1 << 31) + 1), 2, "rows"), (dict(y=None), 1, "output"),
+    (dict(e=None), 1, "tensor scale"), (dict(x=None), 1, "NULL"), (dict(c=None), 1, "NULL"), (dict(s=None), 1, "NULL"),
+    (dict(ldx=56), 2, "ldx"), (dict(ldx=68), 2, "ldx"), (dict(x=FAKE + 2), 6, "aligned"), (dict(c=FAKE + 8), 6, "aligned"),
+    (dict(s=FAKE + 4), 6, "aligned"), (dict(y=FAKE + 2), 6, "aligned"),
+])
+def test_matvec_refusals(L, gated, kw, status, needle):
+    assert mv(L, gated, **kw) == status
+    assert needle in L.bsq_last_error().decode()
+
+
+def test_matvec_types_and_activations(L):
+    assert mv(L, dt=2) == 3
+    assert mv(L, True, act=3) == 3 and mv(L, True, act=-1) == 3
+    for k in ("uc", "us", "ue"):
+        assert mv(L, True, **{k: None}) == 1
+    assert mv(L, True, uc=FAKE + 4) == 6
+
+
+def test_grad_workspace(L):
+    assert L.grad_workspace_bytes(-1) == -1
+    assert L.grad_workspace_bytes((1 << 24) + 1) == -1
+    assert L.grad_workspace_bytes(0) > 0
+    assert L.grad_workspace_bytes(1000) >= L.grad_workspace_bytes(1)
+
+
+def clip(L, sumsq_only=False, **kw):
+    a = dict(p=[FAKE, FAKE], o=None, n=[8, 8], d=[1, 0], count=None, s=FAKE, max_norm=1.0, norm=FAKE, ws=FAKE)
+    a.update(kw)
+    arr = lambda t, v: None if v is None else (t * len(v))(*v)   # noqa: E731
+    count = len(a["p"]) if a["count"] is None else a["count"]
+    P, O, N, D = arr(C.c_void_p, a["p"]), arr(C.c_void_p, a["o"]), arr(C.c_int64, a["n"]), arr(C.c_int, a["d"])
+    if sumsq_only:
+        return L.grad_sumsq(P, N, D, count, a["s"], a["ws"], None)
+    return L.grad_clip(P, O, N, D, count, a["s"], a["max_norm"], a["norm"], None)
+
+
+@pytest.mark.parametrize("sumsq_only", [False, True])
+@pytest.mark.parametrize("kw,status", [
+    (dict(count=-1), 2), (dict(count=(1 << 24) + 1), 2), (dict(n=None), 1), (dict(d=None), 1),
+    (dict(n=[8, -1]), 2), (dict(n=[1 << 40, 1]), 2), (dict(d=[1, 2]), 3), (dict(p=[FAKE, None]), 1),
+    (dict(p=[FAKE + 2, FAKE]), 6), (dict(p=[FAKE, FAKE + 1]), 6), (dict(s=None), 1), (dict(s=FAKE + 4), 6),
+])
+def test_grad_refusals(L, sumsq_only, kw, status):
+    assert clip(L, sumsq_only, **kw) == status
+
+
+def test_grad_only_refusals(L):
+    assert clip(L, True, ws=None) == 1 and clip(L, True, ws=FAKE + 8) == 6
+    assert clip(L, max_norm=-0.5) == 3 and clip(L, max_norm=math.nan) == 3
+    assert clip(L, norm=None) == 1 and clip(L, norm=FAKE + 2) == 6
+    assert clip(L, o=[FAKE, None]) == 1 and clip(L, o=[FAKE, FAKE + 1]) == 6

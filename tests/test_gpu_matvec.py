@@ -1,0 +1,162 @@
+"""nvfp4_matvec and nvfp4_gated_matvec against a plain binary64 form of the decoded weights.
+
+Tolerance: every product of a bf16 token and an exactly decoded weight is exact in fp32, so the sum is
+off by at most (K + 2) 2^-24 S with S = sum |x w| (any order; two more roundings for the division), and
+the output by half a step of its type."""
+import pytest
+import torch
+
+import block_scaled_precision_nvfp4_amd as bsq
+from tests.gpu_common import note
+from tests.plain64 import (act64, assert_within, gated_error, nvfp4_values, product, store_error, sum_error)
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def tokens(M, K, seed, ld=None, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    buf = torch.zeros((M, ld or K), dtype=torch.bfloat16)
+    buf[:, :K] = (torch.randn((M, K), generator=g) * std).to(torch.bfloat16)
+    if ld:
+        buf[:, K:] = float("nan")   # what lies between tokens is not read into any sum
+    return buf.to(DEV)[:, :K]
+
+
+def weights(N, K, seed, rows=False):
+    """Any code and any finite scale byte (subnormal and negative ones among them)."""
+    g = torch.Generator().manual_seed(seed)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8)
+    scales = torch.randint(0, 255, (N, K // 16), generator=g, dtype=torch.uint8)
+    scales[scales == 127] = 126
+    s = torch.rand(N if rows else 1, generator=g) * 900 + 100
+    return codes.to(DEV), scales.to(DEV), s.to(DEV)
+
+
+def check(M, N, K, rows=False, out_dtype=torch.bfloat16, ld=None, seed=1):
+    note("matvec %d %d %d rows=%s %s ld=%s" % (M, N, K, rows, out_dtype, ld))
+    x, w = tokens(M, K, seed, ld), weights(N, K, seed + 1, rows)
+    y = bsq.nvfp4_matvec(x, *w, out_dtype=out_dtype)
+    torch.cuda.synchronize()
+    want, S = product(x.cpu().double(), nvfp4_values(*w))
+    assert_within(y, want, sum_error(K, S) + store_error(want, out_dtype), "y")
+
+
+SIZES = [(1, 1, 16), (1, 16, 128), (1, 17, 48), (2, 33, 144), (3, 256, 256), (1, 300, 4112), (15, 31, 1040),
+         (16, 64, 2048), (17, 64, 528), (33, 47, 2064), (64, 128, 1024), (65, 20, 272), (100, 1030, 640),
+         (1, 2048, 14336)]
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+@pytest.mark.parametrize("rows", [False, True])
+def test_sizes(M, N, K, rows):
+    check(M, N, K, rows)
+    check(M, N, K, rows, torch.float32)
+
+
+def test_strided_tokens():
+    check(5, 100, 272, ld=280)
+    check(40, 64, 1024, ld=2048, out_dtype=torch.float32)
+
+
+def check_gated(act, M, F, K, rows=False, ld=None, seed=3):
+    note("gated matvec act=%d %d %d %d rows=%s" % (act, M, F, K, rows))
+    x, wg, wu = tokens(M, K, seed, ld), weights(F, K, seed + 1, rows), weights(F, K, seed + 2, rows)
+    # bring gate values to the curved part of the activation
+    sg = wg[2] * float((x.float().norm() / M ** 0.5).item()) * 150 / 900
+    h = bsq.nvfp4_gated_matvec(act, x, wg[0], wg[1], sg, *wu)
+    torch.cuda.synchronize()
+    g, Sg = product(x.cpu().double(), nvfp4_values(wg[0], wg[1], sg))
+    u, Su = product(x.cpu().double(), nvfp4_values(*wu))
+    want = act64(g, act)[0] * u
+    e = gated_error(g, u, sum_error(K, Sg), sum_error(K, Su), act)
+    assert_within(h, want, e * (1 + 2.0 ** -8) + store_error(want, torch.bfloat16), "h")
+
+
+@pytest.mark.parametrize("act", [0, 1, 2])
+@pytest.mark.parametrize("M,F,K", [(1, 16, 64), (1, 1033, 2064), (5, 40, 4096), (16, 129, 272), (48, 70, 1040)])
+def test_gated(act, M, F, K):
+    check_gated(act, M, F, K)
+
+
+def test_gated_rows_and_strides():
+    check_gated(0, 3, 65, 528, rows=True)
+    check_gated(2, 20, 33, 160, rows=True, ld=176)
+
+
+def test_empty_and_k0():
+    w = weights(32, 64, 5)
+    y = bsq.nvfp4_matvec(torch.empty((0, 64), dtype=torch.bfloat16, device=DEV), *w)
+    assert tuple(y.shape) == (0, 32)
+    e = [t.to(DEV) for t in (torch.empty((8, 0), dtype=torch.uint8), torch.empty((8, 0), dtype=torch.uint8),
+                             torch.ones(1))]
+    out = torch.full((3, 8), 7.0, dtype=torch.bfloat16, device=DEV)
+    x0 = torch.empty((3, 0), dtype=torch.bfloat16, device=DEV)
+    assert not bsq.nvfp4_matvec(x0, *e, out=out).any()
+    out.fill_(7.0)
+    assert not bsq.nvfp4_gated_matvec(bsq.ACT_SILU, x0, *e, *e, out=out).any()
+
+
+def test_nan_and_infinity_stay_in_their_token_and_row():
+    M, N, K = 6, 40, 272
+    x, (c, s, se) = tokens(M, K, 9).clone(), weights(N, K, 10)
+    x[2, K - 1] = float("nan")
+    x[4, 0] = float("inf")
+    s[7, K // 16 - 1] = 0x7F   # NaN scale in one row, in the block that ends K
+    y = bsq.nvfp4_matvec(x, c, s, se).cpu()
+    bad = torch.isnan(y) | torch.isinf(y)
+    want = torch.zeros_like(bad)
+    want[2, :] = want[4, :] = True
+    want[:, 7] = True
+    assert torch.equal(bad | want, want), "a value outside the NaN's token and row is not finite"
+    assert torch.isnan(y[2]).all() and torch.isnan(y[:, 7]).all() and not torch.isfinite(y[4]).any()
+    clean = bsq.nvfp4_matvec(tokens(M, K, 9), *weights(N, K, 10)).cpu()
+    keep = ~want
+    assert torch.equal(y[keep], clean[keep]), "the other outputs changed"
+
+
+def test_same_bits_out_buffer_and_stream():
+    x, w = tokens(4, 4096, 20), weights(512, 4096, 21)
+    y = bsq.nvfp4_matvec(x, *w)
+    out = torch.empty_like(y)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        assert bsq.nvfp4_matvec(x, *w, out=out) is out
+    side.synchronize()
+    assert torch.equal(out, y)
+
+
+def test_graph_replays():
+    x, w, wu = tokens(1, 1024, 30), weights(256, 1024, 31), weights(256, 1024, 32)
+    y = torch.empty((1, 256), dtype=torch.bfloat16, device=DEV)
+    h = torch.empty_like(y)
+    bsq.nvfp4_matvec(x, *w, out=y)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bsq.nvfp4_matvec(x, *w, out=y)
+        bsq.nvfp4_gated_matvec(bsq.ACT_SILU, x, *w, *wu, out=h)
+    for seed in (41, 42, 43):
+        x.copy_(tokens(1, 1024, seed))
+        want = (bsq.nvfp4_matvec(x, *w), bsq.nvfp4_gated_matvec(bsq.ACT_SILU, x, *w, *wu))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(h, want[1])
+
+
+def test_python_refusals():
+    x, (c, s, se) = tokens(2, 64, 50), weights(8, 64, 51)
+    for bad, exc in [((x.float(), c, s, se), TypeError), ((x[:, :32], c, s, se), ValueError),
+                     ((x, c, s[:, :2].contiguous(), se), ValueError), ((x, c, s, torch.ones(3, device=DEV)), ValueError),
+                     ((x, c.int(), s, se), TypeError), ((x.cpu(), c, s, se), TypeError),
+                     ((torch.empty((64, 2), dtype=torch.bfloat16, device=DEV).t(), c, s, se), ValueError),
+                     ((x.flatten(), c, s, se), ValueError)]:
+        with pytest.raises(exc):
+            bsq.nvfp4_matvec(*bad)
+    with pytest.raises(bsq.BsqError):
+        bsq.nvfp4_gated_matvec(3, x, c, s, se, c, s, se)
+    with pytest.raises(bsq.BsqError):   # a token pitch that is no multiple of 8
+        bsq.nvfp4_matvec(torch.empty((2, 67), dtype=torch.bfloat16, device=DEV)[:, :64], c, s, se)
+    with pytest.raises(ValueError):
+        bsq.nvfp4_matvec(x, c, s, se, out=torch.empty((2, 9), dtype=torch.bfloat16, device=DEV))
