@@ -71,11 +71,15 @@ def lib():
         L.nvfp4_linear_backward.argtypes = [vp, vp, vp, i64, i64, i64, u64, vp, vp, vp, vp, vp]
         L.nvfp4_matvec.argtypes = [i32, i64, i64, i64, vp, i64, vp, vp, vp, vp, i32, vp]
         L.nvfp4_gated_matvec.argtypes = [i32, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.blockscaled_gated_gemm.argtypes = [i32, i32, i64, i64, i64] + [vp] * 12
+        L.blockscaled_gated_gemm_backward.argtypes = [i32, i32, i64, i64, i64] + [vp] * 9
         L.grad_workspace_bytes.argtypes = [i64]
         L.grad_workspace_bytes.restype = C.c_int64
         L.grad_sumsq.argtypes = [vp, vp, vp, i64, vp, vp, vp]
         L.grad_clip.argtypes = [vp, vp, vp, vp, i64, vp, C.c_double, vp, vp]
-        for f in ("nvfp4_matvec", "nvfp4_gated_matvec", "grad_sumsq", "grad_clip", "nvfp4_linear_forward", "nvfp4_linear_backward", "nvfp4_quantize", "nvfp4_quantize_noalloc",
+        for f in ("nvfp4_matvec", "nvfp4_gated_matvec", "blockscaled_gated_gemm", "blockscaled_gated_gemm_backward",
+                  "grad_sumsq", "grad_clip", "nvfp4_linear_forward", "nvfp4_linear_backward", "nvfp4_quantize",
+                  "nvfp4_quantize_noalloc",
                   "nvfp4_col_mxfp8_row_quantize", "nvfp4_quantize_fprop_wgrad", "nvfp4_quantize_rowscaled",
                   "nvfp4_dequantize", "mxfp8_quantize", "mxfp8_requantize_nvfp4", "rht_apply",
                   "blockscaled_gemm", "blockscaled_grouped_gemm", "bsq_version"):
@@ -482,6 +486,81 @@ def nvfp4_gated_matvec(act: int, x: torch.Tensor, gate_codes: torch.Tensor, gate
         gate_scales.data_ptr(), gate_s_enc.data_ptr(), up_codes.data_ptr(), up_scales.data_ptr(),
         up_s_enc.data_ptr(), out.data_ptr(), _stream(dev)))
     return out
+
+
+# ---------------------------------------------------------------- the gated block's products
+
+def _operand(fmt: int, rowscaled: int, codes: torch.Tensor, scales: torch.Tensor, s_enc: Optional[torch.Tensor],
+             name: str, dev):
+    """A quantized operand's checks; returns (rows, K)."""
+    _dev_tensor(codes, torch.uint8, name + "_codes")
+    _dev_tensor(scales, torch.uint8, name + "_scales")
+    nv = (fmt & 0xF) == FMT_NVFP4
+    if codes.dim() != 2:
+        raise ValueError("%s_codes must have two dimensions" % name)
+    rows, K = codes.shape[0], codes.shape[1] * (2 if nv else 1)
+    if tuple(scales.shape) != (rows, K // (16 if nv else 32)):
+        raise ValueError("%s_scales has shape %s for codes %s" % (name, tuple(scales.shape), tuple(codes.shape)))
+    if codes.device != dev or scales.device != dev:
+        raise ValueError("%s must be on %s" % (name, dev))
+    if nv:
+        _dev_tensor(s_enc, torch.float32, name + "_s_enc")
+        want = rows if fmt & rowscaled else 1
+        if s_enc.numel() != want or s_enc.device != dev:
+            raise ValueError("%s_s_enc must hold %d values on %s" % (name, want, dev))
+    return rows, K
+
+
+def blockscaled_gated_gemm(fmt: int, act: int, a_codes: torch.Tensor, a_scales: torch.Tensor,
+                           a_s_enc: Optional[torch.Tensor], gate_codes: torch.Tensor, gate_scales: torch.Tensor,
+                           gate_s_enc: Optional[torch.Tensor], up_codes: torch.Tensor, up_scales: torch.Tensor,
+                           up_s_enc: Optional[torch.Tensor], save_gate_up: bool = False,
+                           out: Optional[torch.Tensor] = None, gate_up: Optional[torch.Tensor] = None):
+    """h = act(A Wg^T) * (A Wu^T) on NVFP4 or MXFP8 operands (``fmt`` and its flags as for ``blockscaled_gemm``; the
+    ``_B`` flags apply to both weights): h [M, F] bf16, or with ``save_gate_up`` (h, gate_up) where gate_up
+    [M, 2F] bf16 holds both projections for ``blockscaled_gated_gemm_backward``.  ``out`` and ``gate_up`` are
+    tensors to write to; new ones are made when none are given."""
+    _dev_tensor(a_codes, torch.uint8, "a_codes")
+    dev = a_codes.device
+    M, K = _operand(fmt, FMT_A_ROWSCALED, a_codes, a_scales, a_s_enc, "a", dev)
+    gate = _operand(fmt, FMT_B_ROWSCALED, gate_codes, gate_scales, gate_s_enc, "gate", dev)
+    up = _operand(fmt, FMT_B_ROWSCALED, up_codes, up_scales, up_s_enc, "up", dev)
+    if gate != up or gate[1] != K:
+        raise ValueError("operands disagree: a [%d, %d], gate %s, up %s" % (M, K, list(gate), list(up)))
+    F = gate[0]
+    h = _output(out, (M, F), torch.bfloat16, dev)
+    if save_gate_up:
+        gate_up = _output(gate_up, (M, 2 * F), torch.bfloat16, dev)
+    elif gate_up is not None:
+        raise ValueError("gate_up is written with save_gate_up only")
+    _check("blockscaled_gated_gemm", lib().blockscaled_gated_gemm(
+        fmt, act, M, F, K, a_codes.data_ptr(), a_scales.data_ptr(), _ptr(a_s_enc), gate_codes.data_ptr(),
+        gate_scales.data_ptr(), _ptr(gate_s_enc), up_codes.data_ptr(), up_scales.data_ptr(), _ptr(up_s_enc),
+        h.data_ptr(), _ptr(gate_up), _stream(dev)))
+    return (h, gate_up) if save_gate_up else h
+
+
+def blockscaled_gated_gemm_backward(fmt: int, act: int, dy_codes: torch.Tensor, dy_scales: torch.Tensor,
+                                    dy_s_enc: Optional[torch.Tensor], w_codes: torch.Tensor, w_scales: torch.Tensor,
+                                    w_s_enc: Optional[torch.Tensor], gate_up: torch.Tensor,
+                                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient [M, 2F] bf16 of ``blockscaled_gated_gemm``'s gate_up from the output gradient dY [M, K] and the
+    down projection's weight [F, K] (both along the block's output): dh = dY Wd^T, d_gate = dh u act'(g),
+    d_up = dh act(g).  ``out`` may be ``gate_up`` itself."""
+    _dev_tensor(dy_codes, torch.uint8, "dy_codes")
+    dev = dy_codes.device
+    M, K = _operand(fmt, FMT_A_ROWSCALED, dy_codes, dy_scales, dy_s_enc, "dy", dev)
+    F, Kw = _operand(fmt, FMT_B_ROWSCALED, w_codes, w_scales, w_s_enc, "w", dev)
+    if Kw != K:
+        raise ValueError("operands disagree on K: dy %d, w %d" % (K, Kw))
+    _dev_tensor(gate_up, torch.bfloat16, "gate_up")
+    if tuple(gate_up.shape) != (M, 2 * F) or gate_up.device != dev:
+        raise ValueError("gate_up must be [%d, %d] on %s, got %s" % (M, 2 * F, dev, tuple(gate_up.shape)))
+    d = _output(out, (M, 2 * F), torch.bfloat16, dev)
+    _check("blockscaled_gated_gemm_backward", lib().blockscaled_gated_gemm_backward(
+        fmt, act, M, F, K, dy_codes.data_ptr(), dy_scales.data_ptr(), _ptr(dy_s_enc), w_codes.data_ptr(),
+        w_scales.data_ptr(), _ptr(w_s_enc), gate_up.data_ptr(), d.data_ptr(), _stream(dev)))
+    return d
 
 
 def _output(out: Optional[torch.Tensor], shape, dtype, dev) -> torch.Tensor:

@@ -19,7 +19,11 @@ struct ActGrad {
     float f, df;
 };
 
-__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+// e^x as the square of e^(x/2): the hardware's exp2 returns 0 for results below 2^-126, the product does not.
+__device__ __forceinline__ float exp_fast(float x) {
+    const float h = __builtin_amdgcn_exp2f(x * 0.721347520f);
+    return h * h;
+}
 
 // s(z) and s(-z); e^-z overflowing gives 0 and, through e^-z / (1 + e^-z), would give NaN for s(-z), so
 // the exponential is always taken of -|z|.
@@ -57,8 +61,9 @@ __device__ __forceinline__ float act_value(float g) {
     if constexpr (ACT == 1) return g * normal_cdf(g);
     float z = g;
     if constexpr (ACT == 2) z = 1.59576912f * __builtin_fmaf(0.044715f * g * g, g, g);
-    // e^-z may overflow to infinity (s = 0) or underflow (s = 1); a NaN passes through
-    return g * __builtin_amdgcn_rcpf(1.0f + exp_fast(-z));
+    // s(z) from e^-|z|, as in sigmoids; a NaN passes through
+    const float e = exp_fast(-__builtin_fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + e);
+    return g * (z >= 0.0f ? r : e * r);
 }
 
 template <int ACT>

@@ -513,6 +513,91 @@ int nvfp4_gated_matvec(int flags, int act, int64_t M, int64_t F, int64_t K, cons
 
 }  // extern "C"
 
+// ---------------------------------------------------------------- the gated block's products
+
+namespace {
+
+// A gated product's format with its flags taken apart.
+struct GatedFmt {
+    int fmt, a_rows, b_rows, slab;
+};
+
+int gated_check(const char* fn, int fmt, int act, int64_t M, int64_t N, int64_t K, GatedFmt& f) {
+    const int flags = BSQ_FMT_A_ROWSCALED | BSQ_FMT_B_ROWSCALED | BSQ_FMT_MX_SLAB;
+    f = GatedFmt{fmt & ~flags, (fmt & BSQ_FMT_A_ROWSCALED) != 0, (fmt & BSQ_FMT_B_ROWSCALED) != 0,
+                 ((fmt & BSQ_FMT_MX_SLAB_A) ? 1 : 0) | ((fmt & BSQ_FMT_MX_SLAB_B) ? 2 : 0)};
+    if (f.fmt != BSQ_FMT_NVFP4 && f.fmt != BSQ_FMT_MXFP8)
+        return fail(BSQ_ERR_ARG, "%s: fmt must be 0 (NVFP4) or 1 (MXFP8), optionally with the row-scaled or slab flags, got %d", fn, fmt);
+    if ((f.a_rows || f.b_rows) && f.fmt != BSQ_FMT_NVFP4) return fail(BSQ_ERR_ARG, "%s: the row-scaled flags apply to NVFP4 operands only", fn);
+    if (f.slab && f.fmt != BSQ_FMT_MXFP8) return fail(BSQ_ERR_ARG, "%s: the slab flags apply to MXFP8 operands only", fn);
+    if (f.slab && K % 512 != 0) return fail(BSQ_ERR_SHAPE, "%s: slab operands need K %% 512 == 0, got %lld", fn, (long long)K);
+    if (bad_act(act)) return fail(BSQ_ERR_ARG, "%s: act must be a BSQ_ACT_* value, got %d", fn, act);
+    if (M < 0 || N < 0 || K < 0) return fail(BSQ_ERR_SHAPE, "%s: negative shape", fn);
+    if (K % 32 != 0) return fail(BSQ_ERR_SHAPE, "%s: K (%lld) must be a multiple of 32", fn, (long long)K);
+    if (K >= gemm_k_limit(f.fmt))
+        return fail(BSQ_ERR_SHAPE, "%s: K (%lld) exceeds %lld", fn, (long long)K, (long long)gemm_k_limit(f.fmt) - 1);
+    if (M > (int64_t)1 << 36 || N > (int64_t)1 << 36 || bsq::gated_tiles(M, N) > 0x7FFFFFFF)
+        return fail(BSQ_ERR_SHAPE, "%s: problem too large for one launch", fn);
+    return BSQ_OK;
+}
+
+int operand_check(const char* fn, const GatedFmt& f, int64_t K, const uint8_t* codes, const uint8_t* scales,
+                  const float* s_enc) {
+    if (K > 0 && (!codes || !scales)) return fail(BSQ_ERR_NULL, "%s: operand pointer is NULL", fn);
+    if (f.fmt == BSQ_FMT_NVFP4 && !s_enc) return fail(BSQ_ERR_NULL, "%s: NVFP4 needs every tensor scale", fn);
+    if (misaligned(codes) || misaligned(scales)) return fail(BSQ_ERR_ALIGN, "%s: device pointers must be 16-byte aligned", fn);
+    return BSQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int blockscaled_gated_gemm(int fmt, int act, int64_t M, int64_t F, int64_t K, const uint8_t* a_codes,
+                           const uint8_t* a_scales, const float* a_s_enc, const uint8_t* gate_codes,
+                           const uint8_t* gate_scales, const float* gate_s_enc, const uint8_t* up_codes,
+                           const uint8_t* up_scales, const float* up_s_enc, void* h, void* gate_up,
+                           void* hip_stream) {
+    static const char* fn = "blockscaled_gated_gemm";
+    GatedFmt f;
+    int st = gated_check(fn, fmt, act, M, F, K, f);
+    if (st) return st;
+    if (M == 0 || F == 0) return ok();
+    if (!h) return fail(BSQ_ERR_NULL, "%s: h is NULL", fn);
+    if (misaligned(h) || misaligned(gate_up)) return fail(BSQ_ERR_ALIGN, "%s: device pointers must be 16-byte aligned", fn);
+    st = operand_check(fn, f, K, a_codes, a_scales, a_s_enc);
+    if (st) return st;
+    st = operand_check(fn, f, K, gate_codes, gate_scales, gate_s_enc);
+    if (st) return st;
+    st = operand_check(fn, f, K, up_codes, up_scales, up_s_enc);
+    if (st) return st;
+    return launched(bsq::launch_gated_gemm(f.fmt, act, M, F, K, a_codes, a_scales, a_s_enc, gate_codes, gate_scales,
+                                           gate_s_enc, up_codes, up_scales, up_s_enc, f.a_rows, f.b_rows, f.slab, h,
+                                           gate_up, hip_stream), fn);
+}
+
+int blockscaled_gated_gemm_backward(int fmt, int act, int64_t M, int64_t F, int64_t K, const uint8_t* dy_codes,
+                                    const uint8_t* dy_scales, const float* dy_s_enc, const uint8_t* w_codes,
+                                    const uint8_t* w_scales, const float* w_s_enc, const void* gate_up,
+                                    void* d_gate_up, void* hip_stream) {
+    static const char* fn = "blockscaled_gated_gemm_backward";
+    GatedFmt f;
+    int st = gated_check(fn, fmt, act, M, F, K, f);
+    if (st) return st;
+    if (M == 0 || F == 0) return ok();
+    if (!gate_up || !d_gate_up) return fail(BSQ_ERR_NULL, "%s: gate_up or d_gate_up is NULL", fn);
+    if (misaligned(gate_up) || misaligned(d_gate_up)) return fail(BSQ_ERR_ALIGN, "%s: device pointers must be 16-byte aligned", fn);
+    st = operand_check(fn, f, K, dy_codes, dy_scales, dy_s_enc);
+    if (st) return st;
+    st = operand_check(fn, f, K, w_codes, w_scales, w_s_enc);
+    if (st) return st;
+    return launched(bsq::launch_gated_gemm_backward(f.fmt, act, M, F, K, dy_codes, dy_scales, dy_s_enc, w_codes,
+                                                    w_scales, w_s_enc, f.a_rows, f.b_rows, f.slab, gate_up, d_gate_up,
+                                                    hip_stream), fn);
+}
+
+}  // extern "C"
+
 // ---------------------------------------------------------------- gradient clipping
 
 namespace {

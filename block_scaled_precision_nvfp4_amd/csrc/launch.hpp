@@ -49,6 +49,18 @@ int launch_nvfp4_matvec(int act, const void* x, int64_t ldx, int64_t M, int64_t 
                         const uint8_t* w_scales, const float* w_s_enc, const uint8_t* up_codes,
                         const uint8_t* up_scales, const float* up_s_enc, int rows, void* y, int y_f32,
                         void* hip_stream);
+// fmt 0 NVFP4, 1 MXFP8; slab bit 0: A's codes, bit 1: the weights' codes are in the slab layout; tiles of the
+// launch (gated_tiles) below 2^31.
+int64_t gated_tiles(int64_t M, int64_t N);
+int launch_gated_gemm(int fmt, int act, int64_t M, int64_t N, int64_t K, const uint8_t* a_codes,
+                      const uint8_t* a_scales, const float* a_s_enc, const uint8_t* gate_codes,
+                      const uint8_t* gate_scales, const float* gate_s_enc, const uint8_t* up_codes,
+                      const uint8_t* up_scales, const float* up_s_enc, int a_rows, int b_rows, int slab, void* h,
+                      void* gate_up, void* hip_stream);
+int launch_gated_gemm_backward(int fmt, int act, int64_t M, int64_t N, int64_t K, const uint8_t* dy_codes,
+                               const uint8_t* dy_scales, const float* dy_s_enc, const uint8_t* w_codes,
+                               const uint8_t* w_scales, const float* w_s_enc, int a_rows, int b_rows, int slab,
+                               const void* gate_up, void* d_gate_up, void* hip_stream);
 int64_t grad_workspace_slots(int64_t count);   // doubles
 int launch_grad_sumsq(const void* const* grads, const int64_t* numels, const int* dtypes, int64_t count,
                       double* sumsq, double* workspace, void* hip_stream);

@@ -446,6 +446,42 @@ int nvfp4_gated_matvec(int flags, int act, int64_t M, int64_t F, int64_t K, cons
                        const uint8_t* up_codes, const uint8_t* up_scales, const float* up_s_enc,
                        void* h, void* hip_stream);
 
+/*
+ * blockscaled_gated_gemm -- the first half of a gated feed-forward block on quantized operands:
+ * g = A Wg^T, u = A Wu^T, h = act(g) u, both products, the activation and the product in one
+ * kernel.  h comes from the unrounded fp32 g and u.
+ *   fmt        as for blockscaled_gemm: NVFP4 or MXFP8, with the row-scaled or the slab flags; the _B
+ *              flags apply to gate and up alike.  act: BSQ_ACT_*.
+ *   a [M][K] (rowwise tokens), gate and up [F][K]: codes, scales and s_enc as for
+ *              blockscaled_gemm's A and B; K % 32 == 0 (slab: 512).
+ *   h          [M][F] bf16 (RNE).
+ *   gate_up    [M][2F] bf16: g in columns 0 .. F-1 and u in F .. 2F-1, which the backward pass needs;
+ *              NULL: not written.
+ *   M, F, K >= 0; M or F 0 writes nothing, K 0 gives zeros.  NVFP4 factors: 1/(S_a S_b) rounded once
+ *   to fp32, or with a row-scaled A the fp32 product of 1/S_a[m] and 1/S_b.
+ */
+int blockscaled_gated_gemm(int fmt, int act, int64_t M, int64_t F, int64_t K,
+                           const uint8_t* a_codes, const uint8_t* a_scales, const float* a_s_enc,
+                           const uint8_t* gate_codes, const uint8_t* gate_scales, const float* gate_s_enc,
+                           const uint8_t* up_codes, const uint8_t* up_scales, const float* up_s_enc,
+                           void* h, void* gate_up, void* hip_stream);
+
+/*
+ * blockscaled_gated_gemm_backward -- its backward pass up to the gradients of the two projections:
+ * dh = dY Wd^T (the down projection's dgrad), d_gate = dh u act'(g), d_up = dh act(g), in one
+ * kernel; dh stays in fp32 and is not stored.
+ *   dy [M][K] rowwise and w [F][K] (the down projection's weight stored along the block's output,
+ *              columnwise): operands, fmt and flags as for blockscaled_gemm's A and B.
+ *   gate_up    [M][2F] bf16, as blockscaled_gated_gemm wrote it.
+ *   d_gate_up  [M][2F] bf16 (RNE): d_gate, then d_up, in the layout of gate_up.  May be gate_up itself.
+ *   Sizes as for blockscaled_gated_gemm.
+ */
+int blockscaled_gated_gemm_backward(int fmt, int act, int64_t M, int64_t F, int64_t K,
+                                    const uint8_t* dy_codes, const uint8_t* dy_scales,
+                                    const float* dy_s_enc, const uint8_t* w_codes,
+                                    const uint8_t* w_scales, const float* w_s_enc,
+                                    const void* gate_up, void* d_gate_up, void* hip_stream);
+
 /* gradient element types */
 #define BSQ_GRAD_BF16 0
 #define BSQ_GRAD_F32 1

@@ -52,13 +52,27 @@ def act64(g, act):
     return g * s, s + g * s * torch.sigmoid(-z) * math.sqrt(8 / math.pi) * (1 + 0.134145 * g * g)
 
 
-# Bound of the device's activation against act64, relative to |act| (or to 1.2 max(1, |g|) e^... for the
-# derivative, see act_tol): the exponential is exp2 of x log2 e, whose argument is rounded to 2^-24 of
+# Bound of the device's activation against act64, relative to |act|: the exponential is exp2 of x log2 e, whose argument is rounded to 2^-24 of
 # |x|; act matters only while it is above 2^-126, where |x| < 88, so e^x is within 88 2^-24 + a few 2^-24
 # < 2^-17 of itself.  The erfc fit adds 2.1e-7 and x^2 its own 2^-24 x^2: the same 2^-17 covers it.
 ACT_REL = 2.0 ** -17
 F32 = 2.0 ** -24
 BF16 = 2.0 ** -8
+
+
+def act_rel(g, act):
+    """Relative error of the device's act(g), and of each term of act'(g), in fp32: the exponential's argument
+    z (g, g^2 / 2 or z(g)) carries at most 8 roundings, each worth |z| 2^-24 of the result; the exponential, the
+    reciprocal and the products after it 10; the fit of the normal distribution function 2.1e-7 < 4 2^-24."""
+    z = g.abs() if act == 0 else (g * g / 2 if act == 1 else math.sqrt(8 / math.pi) * (g + 0.044715 * g ** 3).abs())
+    return (8 * z + 14) * F32
+
+
+def act_grad_terms(g, act):
+    """Sum of the magnitudes of act'(g)'s terms, which may cancel."""
+    f, d = act64(g, act)
+    s = torch.where(g == 0, torch.full_like(g, 0.5), f / torch.where(g == 0, torch.ones_like(g), g))
+    return s.abs() + (d - s).abs()
 
 
 def product(a, b):

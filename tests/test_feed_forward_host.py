@@ -85,3 +85,46 @@ def test_grad_only_refusals(L):
     assert clip(L, max_norm=-0.5) == 3 and clip(L, max_norm=math.nan) == 3
     assert clip(L, norm=None) == 1 and clip(L, norm=FAKE + 2) == 6
     assert clip(L, o=[FAKE, None]) == 1 and clip(L, o=[FAKE, FAKE + 1]) == 6
+
+
+def gated(L, backward=False, **kw):
+    a = dict(fmt=0, act=0, M=4, F=64, K=512, a=FAKE, as_=FAKE, ae=FAKE, g=FAKE, gs=FAKE, ge=FAKE, u=FAKE, us=FAKE,
+             ue=FAKE, h=FAKE, gu=FAKE)
+    a.update(kw)
+    if backward:
+        return L.blockscaled_gated_gemm_backward(a["fmt"], a["act"], a["M"], a["F"], a["K"], a["a"], a["as_"], a["ae"],
+                                                 a["g"], a["gs"], a["ge"], a["gu"], a["h"], None)
+    return L.blockscaled_gated_gemm(a["fmt"], a["act"], a["M"], a["F"], a["K"], a["a"], a["as_"], a["ae"], a["g"],
+                                    a["gs"], a["ge"], a["u"], a["us"], a["ue"], a["h"], a["gu"], None)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("kw,status,needle", [
+    (dict(fmt=2), 3, "fmt"), (dict(fmt=0x11), 3, "row-scaled"), (dict(fmt=0x40), 3, "slab"),
+    (dict(fmt=0xC1, K=544), 2, "512"), (dict(act=3), 3, "act"), (dict(act=-1), 3, "act"), (dict(M=-1), 2, "negative"),
+    (dict(F=-1), 2, "negative"), (dict(K=-32), 2, "negative"), (dict(K=48), 2, "multiple of 32"),
+    (dict(K=1 << 24), 2, "exceeds"), (dict(fmt=1, K=1 << 23), 2, "exceeds"), (dict(M=1 << 30, F=1 << 30), 2, "large"),
+    (dict(M=1 << 62, F=8), 2, "large"), (dict(h=None), 1, "NULL"), (dict(h=FAKE + 8), 6, "aligned"),
+    (dict(gu=FAKE + 2), 6, "aligned"), (dict(a=None), 1, "NULL"), (dict(as_=None), 1, "NULL"), (dict(ae=None), 1, "scale"),
+    (dict(g=None), 1, "NULL"), (dict(ge=None), 1, "scale"), (dict(g=FAKE + 4), 6, "aligned"), (dict(gs=FAKE + 8), 6, "aligned"),
+])
+def test_gated_refusals(L, backward, kw, status, needle):
+    assert gated(L, backward, **kw) == status
+    assert needle in L.bsq_last_error().decode()
+
+
+def test_gated_only_refusals(L):
+    assert gated(L, u=None) == 1 and gated(L, ue=None) == 1 and gated(L, us=FAKE + 1) == 6
+    assert gated(L, True, gu=None) == 1
+    assert gated(L, M=0, h=None) == 0 and gated(L, True, F=0, gu=None) == 0   # nothing to do
+
+
+@pytest.mark.parametrize("act", [0, 1, 2])
+def test_plain_derivatives_against_differences(act):
+    import torch
+
+    from tests.plain64 import act64
+    g = torch.linspace(-12, 12, 2001, dtype=torch.float64)
+    e = 1e-5
+    d = (act64(g + e, act)[0] - act64(g - e, act)[0]) / (2 * e)
+    assert float((d - act64(g, act)[1]).abs().max()) < 1e-8
