@@ -11,6 +11,8 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from array import array
+from operator import attrgetter
 from typing import Dict, Optional, Sequence
 
 import torch
@@ -77,8 +79,9 @@ def lib():
         L.grad_workspace_bytes.restype = C.c_int64
         L.grad_sumsq.argtypes = [vp, vp, vp, i64, vp, vp, vp]
         L.grad_clip.argtypes = [vp, vp, vp, vp, i64, vp, C.c_double, vp, vp]
+        L.clip_grad_norm.argtypes = [vp, vp, vp, vp, i64, C.c_double, vp, vp, vp]
         for f in ("nvfp4_matvec", "nvfp4_gated_matvec", "blockscaled_gated_gemm", "blockscaled_gated_gemm_backward",
-                  "grad_sumsq", "grad_clip", "nvfp4_linear_forward", "nvfp4_linear_backward", "nvfp4_quantize",
+                  "grad_sumsq", "grad_clip", "clip_grad_norm", "nvfp4_linear_forward", "nvfp4_linear_backward", "nvfp4_quantize",
                   "nvfp4_quantize_noalloc",
                   "nvfp4_col_mxfp8_row_quantize", "nvfp4_quantize_fprop_wgrad", "nvfp4_quantize_rowscaled",
                   "nvfp4_dequantize", "mxfp8_quantize", "mxfp8_requantize_nvfp4", "rht_apply",
@@ -578,64 +581,84 @@ def _output(out: Optional[torch.Tensor], shape, dtype, dev) -> torch.Tensor:
 # ---------------------------------------------------------------- gradient clipping
 
 _GRAD_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+_device_of, _dtype_of = attrgetter("device"), attrgetter("dtype")
+
+
+def _list_check(tensors: list, name: str, dev):
+    """Explains what is wrong with a list of gradients (only called when something is)."""
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s %d must be a tensor" % (name, i))
+        if not t.is_cuda or t.device != dev:
+            raise ValueError("%s %d must be on %s, a GPU" % (name, i, dev))
+        if t.dtype not in _GRAD_DTYPES:
+            raise TypeError("%s %d must be bfloat16 or float32, got %s" % (name, i, t.dtype))
+        if not t.is_contiguous():
+            raise ValueError("%s %d must be contiguous" % (name, i))
 
 
 class _GradList:
-    """A list of gradients (and outputs) as the C ABI's host arrays."""
+    """A list of gradients (and outputs) as the C ABI's host arrays.  Models have hundreds of them, so each
+    property is taken over the whole list at once."""
 
     def __init__(self, grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None):
         grads = list(grads)
         if not grads:
             raise ValueError("the list of gradients is empty")
-        n = len(grads)
-        dev = grads[0].device
-        for i, t in enumerate(grads):
-            if not t.is_cuda or t.device != dev:
-                raise ValueError("gradient %d must be on %s, a GPU" % (i, dev))
-            if t.dtype not in _GRAD_DTYPES:
-                raise TypeError("gradient %d must be bfloat16 or float32, got %s" % (i, t.dtype))
-            if not t.is_contiguous():
-                raise ValueError("gradient %d must be contiguous" % i)
+        dev = getattr(grads[0], "device", None)
+        self.ptrs, self.numels, self.dtypes = self._arrays(grads, "gradient", dev)
         self.outs = None
         if out is not None:
             out = list(out)
-            if len(out) != n:
-                raise ValueError("out has %d tensors for %d gradients" % (len(out), n))
-            for i, (t, o) in enumerate(zip(grads, out)):
-                if o.dtype != t.dtype or o.shape != t.shape or o.device != dev or not o.is_contiguous():
-                    raise ValueError("out[%d] must be a contiguous tensor like its gradient" % i)
-            self.outs = (C.c_void_p * n)(*[t.data_ptr() for t in out])
-        self.n, self.device = n, dev
-        self.ptrs = (C.c_void_p * n)(*[t.data_ptr() for t in grads])
-        self.numels = (C.c_int64 * n)(*[t.numel() for t in grads])
-        self.dtypes = (C.c_int * n)(*[_GRAD_DTYPES[t.dtype] for t in grads])
+            if len(out) != len(grads):
+                raise ValueError("out has %d tensors for %d gradients" % (len(out), len(grads)))
+            self.outs, numels, dtypes = self._arrays(out, "out", dev)
+            if numels != self.numels or dtypes != self.dtypes:
+                i = next(i for i in range(len(out)) if numels[i] != self.numels[i] or dtypes[i] != self.dtypes[i])
+                raise ValueError("out[%d] must have its gradient's type and number of elements" % i)
+        self.n, self.device = len(grads), dev
 
-    def sumsq(self, workspace: Optional[torch.Tensor]) -> torch.Tensor:
-        s = torch.empty(1, dtype=torch.float64, device=self.device)
-        ws = _workspace(workspace, lib().grad_workspace_bytes(self.n), self.device)
-        _check("grad_sumsq", lib().grad_sumsq(self.ptrs, self.numels, self.dtypes, self.n, s.data_ptr(),
-                                              ws.data_ptr(), _stream(self.device)))
-        return s
+    @staticmethod
+    def _arrays(tensors: list, name: str, dev):
+        try:
+            kinds = array("i", map(_GRAD_DTYPES.__getitem__, map(_dtype_of, tensors)))
+            good = (dev.type == "cuda" and all(map(dev.__eq__, map(_device_of, tensors)))
+                    and all(map(torch.Tensor.is_contiguous, tensors)))
+        except (AttributeError, KeyError, TypeError):
+            good = False
+        if not good:
+            _list_check(tensors, name, dev)
+        return array("Q", map(torch.Tensor.data_ptr, tensors)), array("q", map(torch.Tensor.numel, tensors)), kinds
 
-    def clip(self, sumsq: torch.Tensor, max_norm: float) -> torch.Tensor:
-        _dev_tensor(sumsq, torch.float64, "sumsq")
-        norm = torch.empty(1, dtype=torch.float32, device=self.device)
-        _check("grad_clip", lib().grad_clip(self.ptrs, self.outs, self.numels, self.dtypes, self.n, sumsq.data_ptr(),
-                                            float(max_norm), norm.data_ptr(), _stream(self.device)))
-        return norm
+    def args(self, outs: bool = True):
+        at = lambda a: None if a is None else a.buffer_info()[0]   # noqa: E731
+        return (at(self.ptrs), *((at(self.outs),) if outs else ()), at(self.numels), at(self.dtypes), self.n)
+
+    def workspace(self, workspace: Optional[torch.Tensor]) -> torch.Tensor:
+        return _workspace(workspace, lib().grad_workspace_bytes(self.n), self.device)
 
 
 def grad_sumsq(grads: Sequence[torch.Tensor], workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The sum of squares over all gradients (bf16 and float32 tensors) as a float64[1] device tensor; ranks
     that hold different gradients add theirs up before ``grad_clip``."""
-    return _GradList(grads).sumsq(workspace)
+    g = _GradList(grads)
+    ws = g.workspace(workspace)
+    sumsq = torch.empty(1, dtype=torch.float64, device=g.device)
+    _check("grad_sumsq", lib().grad_sumsq(*g.args(False), sumsq.data_ptr(), ws.data_ptr(), _stream(g.device)))
+    return sumsq
 
 
 def grad_clip(grads: Sequence[torch.Tensor], sumsq: torch.Tensor, max_norm: float,
               out: Optional[Sequence[torch.Tensor]] = None) -> torch.Tensor:
-    """Scales the gradients by min(1, max_norm / (sqrt(sumsq) + 1e-6)), in place or into ``out``; returns the
-    norm as a float32[1] device tensor."""
-    return _GradList(grads, out).clip(sumsq, max_norm)
+    """Scales the gradients by min(1, max_norm / (sqrt(sumsq) + 1e-6)), in place or into ``out`` (tensors of the
+    gradients' types and sizes); returns the norm as a float32[1] device tensor."""
+    g = _GradList(grads, out)
+    _dev_tensor(sumsq, torch.float64, "sumsq")
+    if sumsq.numel() != 1 or sumsq.device != g.device:
+        raise ValueError("sumsq must hold one value on %s" % (g.device,))
+    norm = torch.empty(1, dtype=torch.float32, device=g.device)
+    _check("grad_clip", lib().grad_clip(*g.args(), sumsq.data_ptr(), max_norm, norm.data_ptr(), _stream(g.device)))
+    return norm
 
 
 def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None,
@@ -644,4 +667,8 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
     exceed ``max_norm``, in place or into ``out``.  ``workspace``: at least grad_workspace_bytes(len(grads))
     bytes of scratch; one is allocated when none is given."""
     g = _GradList(grads, out)
-    return g.clip(g.sumsq(workspace), max_norm)
+    ws = g.workspace(workspace)
+    norm = torch.empty(1, dtype=torch.float32, device=g.device)
+    _check("clip_grad_norm", lib().clip_grad_norm(*g.args(), max_norm, norm.data_ptr(), ws.data_ptr(),
+                                                  _stream(g.device)))
+    return norm

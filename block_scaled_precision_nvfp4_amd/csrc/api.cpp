@@ -656,4 +656,17 @@ int grad_clip(const void* const* grads, void* const* outs, const int64_t* numels
     return launched(bsq::launch_grad_clip(grads, outs, numels, dtypes, count, sumsq, max_norm, norm, hip_stream), fn);
 }
 
+int clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes,
+                   int64_t count, double max_norm, float* norm, void* workspace, void* hip_stream) {
+    static const char* fn = "clip_grad_norm";
+    if (!(max_norm >= 0.0)) return fail(BSQ_ERR_ARG, "%s: max_norm must not be negative or NaN", fn);
+    const int st = grads_check(fn, grads, outs, numels, dtypes, count);
+    if (st) return st;
+    if (!norm || !workspace) return fail(BSQ_ERR_NULL, "%s: norm or workspace is NULL", fn);
+    if (misaligned(workspace) || (reinterpret_cast<uintptr_t>(norm) & 3u))
+        return fail(BSQ_ERR_ALIGN, "%s: norm or workspace is not aligned", fn);
+    return launched(bsq::launch_clip_grad_norm(grads, outs, numels, dtypes, count, max_norm, norm,
+                                               static_cast<double*>(workspace), hip_stream), fn);
+}
+
 }  // extern "C"

@@ -66,6 +66,8 @@ int launch_grad_sumsq(const void* const* grads, const int64_t* numels, const int
                       double* sumsq, double* workspace, void* hip_stream);
 int launch_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes,
                      int64_t count, const double* sumsq, double max_norm, float* norm, void* hip_stream);
+int launch_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes,
+                          int64_t count, double max_norm, float* norm, double* workspace, void* hip_stream);
 const char* hip_error_string(int e);
 
 }  // namespace bsq

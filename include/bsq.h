@@ -487,10 +487,11 @@ int blockscaled_gated_gemm_backward(int fmt, int act, int64_t M, int64_t F, int6
 #define BSQ_GRAD_F32 1
 
 /*
- * grad_sumsq / grad_clip -- the global 2-norm of a list of gradients, and the gradients scaled so
+ * grad_sumsq / grad_clip / clip_grad_norm -- the global 2-norm of a list of gradients, and the gradients scaled so
  * that it does not exceed max_norm: N = sqrt(sum of all squares), c = min(1, max_norm / (N +
  * 1e-6)), out = c * grad rounded once (RNE) to the gradient's type.  Two calls, so that ranks that
- * hold different gradients can add up their sums in between.
+ * hold different gradients can add up their sums in between; clip_grad_norm is both in one, with
+ * the same results and one launch less.
  *   grads, outs, numels, dtypes  HOST arrays of count entries, read before the call returns:
  *              device pointers (aligned to their elements; tensors may start anywhere in a flat
  *              bucket), element counts (0 allowed; at most 2^40 in all), BSQ_GRAD_*.  outs NULL:
@@ -507,6 +508,9 @@ int grad_sumsq(const void* const* grads, const int64_t* numels, const int* dtype
                double* sumsq, void* workspace, void* hip_stream);
 int grad_clip(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes,
               int64_t count, const double* sumsq, double max_norm, float* norm, void* hip_stream);
+
+int clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes,
+                   int64_t count, double max_norm, float* norm, void* workspace, void* hip_stream);
 
 /* Message of the last failing call on this thread ("" if none).  Host memory owned
  * by the library; valid until the thread's next call. */
