@@ -468,7 +468,7 @@ int matvec_check(const char* fn, int flags, int64_t M, int64_t N, int64_t K, con
     if (K >= gemm_k_limit(BSQ_FMT_NVFP4))
         return fail(BSQ_ERR_SHAPE, "%s: K (%lld) exceeds %lld", fn, (long long)K, (long long)gemm_k_limit(BSQ_FMT_NVFP4) - 1);
     if (M > (int64_t)1 << 20) return fail(BSQ_ERR_SHAPE, "%s: %lld tokens exceed 2^20", fn, (long long)M);
-    if (N > (int64_t)1 << 31) return fail(BSQ_ERR_SHAPE, "%s: %lld weight rows exceed 2^31", fn, (long long)N);
+    if (N > (int64_t)1 << 27) return fail(BSQ_ERR_SHAPE, "%s: %lld weight rows exceed 2^27", fn, (long long)N);
     if (M == 0 || N == 0) return BSQ_OK;
     if (!y) return fail(BSQ_ERR_NULL, "%s: the output is NULL", fn);
     if (!s_enc) return fail(BSQ_ERR_NULL, "%s: NVFP4 needs its tensor scale", fn);

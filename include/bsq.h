@@ -425,7 +425,7 @@ int nvfp4_linear_backward(const void* dy, const void* w, const void* saved, int6
  *   x       bf16, row m at x + m * ldx elements; ldx >= K, ldx % 8 == 0.
  *   w_codes [N][K/2], w_scales [N][K/16]: rowwise NVFP4 as nvfp4_quantize writes it.  K % 16 == 0.
  *   y       [M][N], y_dtype BSQ_OUT_BF16 (RNE) or BSQ_OUT_F32.
- *   M in [0, 2^20], N >= 0, K >= 0 below 2^24; M or N 0 writes nothing, K 0 writes zeros.  Any M is computed;
+ *   M in [0, 2^20], N in [0, 2^27], K >= 0 below 2^24; M or N 0 writes nothing, K 0 writes zeros.  Any M is computed;
  *   from some 64 tokens on, quantizing them and calling blockscaled_gemm is faster.
  * A NaN or an infinity in a token reaches that token's outputs only, one in a row's scales that
  * output column only.  The result does not depend on the order in which the GPU runs the work.
