@@ -5,9 +5,8 @@
 //   gelu       act(g) = g P(g),         P(g) = erfc(-g / sqrt 2) / 2
 //   gelu_tanh  act(g) = g s(z(g)),      z(g) = sqrt(8/pi) (g + 0.044715 g^3)
 //
-// (0.5 (1 + tanh y) = s(2 y), so the last is the usual tanh form.)  Each is written so that no two
-// nearly equal values are subtracted: the results keep their relative accuracy where act(g) is tiny
-// (g far below zero), and 1 - s is taken as s(-z).
+// (0.5 (1 + tanh y) = s(2 y), so the last is the usual tanh form.)  Each keeps its relative accuracy where
+// act(g) is tiny (g far below zero).
 #pragma once
 
 #include "device_common.hpp"
@@ -25,15 +24,10 @@ __device__ __forceinline__ float exp_fast(float x) {
     return h * h;
 }
 
-// s(z) and s(-z); e^-z overflowing gives 0 and, through e^-z / (1 + e^-z), would give NaN for s(-z), so
-// the exponential is always taken of -|z|.
-__device__ __forceinline__ void sigmoids(float z, float& s, float& sn) {
-    const float e = exp_fast(-__builtin_fabsf(z));
-    const float r = __builtin_amdgcn_rcpf(1.0f + e);
-    const float small = e * r;
-    s = z >= 0.0f ? r : small;
-    sn = z >= 0.0f ? small : r;
-    if (z != z) s = sn = z;
+// s(z), from e^-|z| so that nothing overflows; a NaN passes through.
+__device__ __forceinline__ float sigmoid(float z) {
+    const float e = exp_fast(-__builtin_fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + e);
+    return z >= 0.0f ? r : e * r;
 }
 
 // P(g) = erfc(-g / sqrt 2) / 2, the normal distribution function.  With x = |g| / sqrt 2 and t = 1 / (1 +
@@ -61,9 +55,7 @@ __device__ __forceinline__ float act_value(float g) {
     if constexpr (ACT == 1) return g * normal_cdf(g);
     float z = g;
     if constexpr (ACT == 2) z = 1.59576912f * __builtin_fmaf(0.044715f * g * g, g, g);
-    // s(z) from e^-|z|, as in sigmoids; a NaN passes through
-    const float e = exp_fast(-__builtin_fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + e);
-    return g * (z >= 0.0f ? r : e * r);
+    return g * sigmoid(z);
 }
 
 template <int ACT>
@@ -75,12 +67,13 @@ __device__ __forceinline__ ActGrad act_grad(float g) {
     float z = g, dz = 1.0f;
     if constexpr (ACT == 2) {
         z = 1.59576912f * __builtin_fmaf(0.044715f * g * g, g, g);
-        // kept finite, so that it stays without effect where s(z) s(-z) is 0
+        // kept finite, so that it stays without effect where s (1 - s) is 0
         dz = __builtin_fminf(1.59576912f * __builtin_fmaf(0.134145f * g, g, 1.0f), 3.0e38f);
     }
-    float s, sn;
-    sigmoids(z, s, sn);
-    return {g * s, __builtin_fmaf(g * s * sn, dz, s)};
+    // act'(g) = s + g s s(-z) dz.  s(-z) as 1 - s: where s is near 1 that is off by 2^-24, which the s it is added
+    // to outweighs, and where s is small it is exact to rounding.
+    const float s = sigmoid(z), f = g * s;
+    return {f, __builtin_fmaf(f * (1.0f - s), dz, s)};
 }
 
 }  // namespace bsq

@@ -15,6 +15,15 @@
 
 namespace bsq {
 
+// Eight bf16 values at any multiple of an element (rows of tensors whose width is no multiple of 8).
+struct __attribute__((packed, aligned(2))) Bf16x8Any { uint32_t w[4]; };
+
+__device__ __forceinline__ u32x4s load_any(const uint16_t* p) {
+    const Bf16x8Any v = *(const Bf16x8Any*)p;
+    return u32x4s{v.w[0], v.w[1], v.w[2], v.w[3]};
+}
+__device__ __forceinline__ void store_any(uint16_t* p, u32x4s v) { *(Bf16x8Any*)p = Bf16x8Any{{v.x, v.y, v.z, v.w}}; }
+
 // Calls body(std::integral_constant<int, ACT>) for the run-time act.
 template <class F>
 __device__ __forceinline__ void with_act(int act, F&& body) {
@@ -57,15 +66,14 @@ __device__ __forceinline__ void gated_factors(const GatedArgs& g, int64_t m0, in
 
 // One tile per workgroup: 256 rows of A by 128 columns of h.  Epilogue in two passes of 64 rows per
 // wave: g, u and h are formed where the accumulators are and staged in the wave's own LDS region as
-// three row-major blocks of 64 columns, then stored in 16-byte chunks (single elements where the rows
-// of h do not keep 16-byte chunks apart).
+// three row-major blocks of 64 columns, then stored in 16-byte chunks.
 template <int FMT, int MODE = 0, int SL = 0>
 __global__ __launch_bounds__(256, 1) void gated_kernel(GatedArgs g) {
     using F = Fmt<FMT>;
     constexpr int RS = 3 * 128 + 16;   // staged bytes of a row: h, gate, up
     static_assert(4 * 64 * RS <= F::LDS - FACT_BYTES, "epilogue staging");
     __shared__ __attribute__((aligned(16))) uint8_t lds[F::LDS];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int wm = (wave >> 1) * 128, wn = (wave & 1) * 128;
     int64_t tm, tn;
     tile_of((g.M + GBM - 1) / GBM, (g.N + GBN / 2 - 1) / (GBN / 2), blockIdx.x, tm, tn);
@@ -127,9 +135,17 @@ __global__ __launch_bounds__(256, 1) void gated_kernel(GatedArgs g) {
                         if (r0 + row < g.M && c0 + 8 * c < g.N) *(uint4*)(out + (r0 + row) * pitch + c0 + 8 * c) = v;
                     }
                 } else {
-                    for (int row = 0; row < 64; ++row)
-                        if (r0 + row < g.M && c0 + lane < g.N)
-                            out[(r0 + row) * pitch + c0 + lane] = *(const uint16_t*)(reg + row * RS + 128 * o + 2 * lane);
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) {
+                        const int row = 8 * p + (lane >> 3), c = 8 * (lane & 7);
+                        const uint4 v = *(const uint4*)(reg + row * RS + 128 * o + 2 * c);
+                        uint16_t* dst = out + (r0 + row) * pitch + c0 + c;
+                        if (r0 + row >= g.M) continue;
+                        if (c0 + c + 8 <= g.N) store_any(dst, u32x4s{v.x, v.y, v.z, v.w});
+                        else
+                            for (int e = 0; c0 + c + e < g.N; ++e)   // the chunk that N ends in
+                                dst[e] = *(const uint16_t*)(reg + row * RS + 128 * o + 2 * (c + e));
+                    }
                 }
             }
             asm volatile("" ::: "memory");
@@ -144,16 +160,29 @@ struct GatedBackArgs : GemmArgs {   // c: the gradient of [gate, up], [M][2N] bf
     int act;
 };
 
+// Both gradients of 8 columns of a row (bf16 pairs) from dh and their gate and up.
+template <int ACT>
+__device__ __forceinline__ void gated_grads(const float (&dh)[8], u32x4s gate, u32x4s up, u32x4s& dg, u32x4s& du) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const ActGrad a = act_grad<ACT>(bf16_lo(gate[e])), b = act_grad<ACT>(bf16_hi(gate[e]));
+        dg[e] = bf16x2_rne(dh[2 * e] * bf16_lo(up[e]) * a.df, dh[2 * e + 1] * bf16_hi(up[e]) * b.df);
+        du[e] = bf16x2_rne(dh[2 * e] * a.f, dh[2 * e + 1] * b.f);
+    }
+}
+
 // One tile per workgroup: 256 x 256 of dh.  Epilogue in two passes of 64 rows per wave: dh goes through the
 // wave's own LDS region in fp32, then each lane takes 8 columns of a row, reads their gate and up (16
-// bytes each) and writes both gradients.
+// bytes each) and writes both gradients.  The tile's 512 KiB of gate, up and gradients are a third of the
+// kernel's time, so gate and up are asked for 32 rows ahead of their use (64 registers that the K loop no
+// longer needs), and the writes wait for nobody.
 template <int FMT, int MODE = 0, int SL = 0>
 __global__ __launch_bounds__(256, 1) void gated_backward_kernel(GatedBackArgs g) {
     using F = Fmt<FMT>;
     constexpr int RS = 128 * 4 + 16;
     static_assert(4 * 64 * RS <= F::LDS - FACT_BYTES, "epilogue staging");
     __shared__ __attribute__((aligned(16))) uint8_t lds[F::LDS];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int wm = (wave >> 1) * 128, wn = (wave & 1) * 128;
     int64_t tm, tn;
     tile_of((g.M + GBM - 1) / GBM, (g.N + GBN - 1) / GBN, blockIdx.x, tm, tn);
@@ -169,9 +198,42 @@ __global__ __launch_bounds__(256, 1) void gated_backward_kernel(GatedBackArgs g)
     }
     const int frow = lane & 31, kh = lane >> 5;
     uint8_t* reg = lds + wave * 64 * RS;
-    const bool chunks = g.N % 8 == 0;   // uniform
-    with_act(g.act, [&](auto act_c) {
+    // 16-byte chunks of rows, whole inside or outside the tensors, within a buffer resource
+    const bool chunks = g.N % 8 == 0 && g.N < (int64_t)1 << 20;   // uniform
+    // the wave's rows of gate_up and of the gradient; a chunk outside them gets an offset out of range
+    const int64_t rows = tile_rows(g.M - m0 - wm, 128), c0 = n0 + wn;
+    const uint32_t pitch = (uint32_t)(4 * g.N), half = (uint32_t)(2 * g.N);
+    const __amdgpu_buffer_rsrc_t in = make_rsrc((const uint8_t*)g.gate_up + (m0 + wm) * 4 * g.N, rows * 4 * g.N);
+    const __amdgpu_buffer_rsrc_t out = make_rsrc((const uint8_t*)g.c + (m0 + wm) * 4 * g.N, rows * 4 * g.N);
+    const int col = 8 * (lane & 15);
+    const uint32_t off0 = c0 + col < g.N ? (uint32_t)(lane >> 4) * pitch + (uint32_t)(2 * (c0 + col)) : OOB;
+    const uint32_t step = off0 == OOB ? 0u : pitch;
+    auto at = [&](int row4) { return off0 + (uint32_t)row4 * step; };   // row4 + lane / 16
+    // tensors whose rows do not keep chunks whole: plain loads and stores of the whole chunks, and elements
+    // where N ends inside one
+    const int64_t left = g.N - c0 - col, i0 = (m0 + wm + (lane >> 4)) * 2 * g.N + c0 + col;
+    auto whole = [&](int row4) { return left >= 8 && row4 + (lane >> 4) < rows; };
+    auto epilogue = [&](auto act_c, auto chunks_c) {
         constexpr int ACT = decltype(act_c)::value;
+        constexpr bool CHUNKS = decltype(chunks_c)::value;
+        u32x4s gate[2][8], up[2][8];   // of 32 rows each
+        auto fetch = [&](auto b_c) {
+            constexpr int B = decltype(b_c)::value;
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                if constexpr (CHUNKS) {
+                    const uint32_t o = at(32 * B + 4 * p);
+                    gate[B & 1][p] = __builtin_amdgcn_raw_buffer_load_b128(in, (int)o, 0, 0);
+                    up[B & 1][p] = __builtin_amdgcn_raw_buffer_load_b128(in, (int)o, (int)half, 0);
+                } else if (whole(32 * B + 4 * p)) {
+                    const uint16_t* src = g.gate_up + i0 + (int64_t)(32 * B + 4 * p) * 2 * g.N;
+                    gate[B & 1][p] = load_any(src);
+                    up[B & 1][p] = load_any(src + g.N);
+                }
+            }
+            asm volatile("" ::: "memory");
+        };
+        fetch(std::integral_constant<int, 0>{});
         static_for<0, 2>([&](auto h_c) {
             constexpr int H = decltype(h_c)::value;
             static_for<0, 8>([&](auto t_c) {
@@ -179,56 +241,59 @@ __global__ __launch_bounds__(256, 1) void gated_backward_kernel(GatedBackArgs g)
                 [[maybe_unused]] const float fr = F::NV ? fa[wm + 32 * I + frow] : 1.0f;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int col = 32 * J + 8 * q + 4 * kh;
+                    const int c = 32 * J + 8 * q + 4 * kh;
                     float4 v = make_float4(acc[I][J][4 * q], acc[I][J][4 * q + 1], acc[I][J][4 * q + 2],
                                            acc[I][J][4 * q + 3]);
                     if constexpr (F::NV) {
-                        const float* f = fb + wn + col;
+                        const float* f = fb + wn + c;
                         v.x *= fr * f[0]; v.y *= fr * f[1]; v.z *= fr * f[2]; v.w *= fr * f[3];
                     }
-                    *(float4*)(reg + (32 * IL + frow) * RS + 4 * col) = v;
+                    *(float4*)(reg + (32 * IL + frow) * RS + 4 * c) = v;
                 }
                 __builtin_amdgcn_sched_barrier(0);
             });
             asm volatile("" ::: "memory");
-            const int64_t r0 = m0 + wm + 64 * H, c0 = n0 + wn;
-            uint16_t* out = (uint16_t*)g.c;
-            if (chunks) {
-#pragma unroll 4
-                for (int p = 0; p < 16; ++p) {
-                    const int row = 4 * p + (lane >> 4), c = 8 * (lane & 15);
-                    if (r0 + row >= g.M || c0 + c >= g.N) continue;
-                    const int64_t at = (r0 + row) * 2 * g.N + c0 + c;
-                    float gv[8], uv[8], dh[8];
-                    unpack_bf16x8(*(const uint4*)(g.gate_up + at), gv);
-                    unpack_bf16x8(*(const uint4*)(g.gate_up + at + g.N), uv);
-                    *(float4*)dh = *(const float4*)(reg + row * RS + 4 * c);
-                    *(float4*)(dh + 4) = *(const float4*)(reg + row * RS + 4 * c + 16);
-                    uint32_t dg[4], du[4];
+            static_for<0, 2>([&](auto b_c) {
+                constexpr int B = 2 * H + decltype(b_c)::value;   // 32 rows
+                if constexpr (B < 3) fetch(std::integral_constant<int, B + 1>{});
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const ActGrad a = act_grad<ACT>(gv[2 * e]), b = act_grad<ACT>(gv[2 * e + 1]);
-                        dg[e] = bf16x2_rne(dh[2 * e] * uv[2 * e] * a.df, dh[2 * e + 1] * uv[2 * e + 1] * b.df);
-                        du[e] = bf16x2_rne(dh[2 * e] * a.f, dh[2 * e + 1] * b.f);
+                for (int p = 0; p < 8; ++p) {
+                    const uint8_t* src = reg + (32 * (B & 1) + 4 * p + (lane >> 4)) * RS + 4 * col;
+                    float dh[8];
+                    *(float4*)dh = *(const float4*)src;
+                    *(float4*)(dh + 4) = *(const float4*)(src + 16);
+                    u32x4s dg, du;
+                    gated_grads<ACT>(dh, gate[B & 1][p], up[B & 1][p], dg, du);
+                    if constexpr (CHUNKS) {
+                        const uint32_t o = at(32 * B + 4 * p);
+                        __builtin_amdgcn_raw_buffer_store_b128(dg, out, (int)o, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(du, out, (int)o, (int)half, 0);
+                    } else if (whole(32 * B + 4 * p)) {
+                        uint16_t* dst = (uint16_t*)g.c + i0 + (int64_t)(32 * B + 4 * p) * 2 * g.N;
+                        store_any(dst, dg);
+                        store_any(dst + g.N, du);
                     }
-                    *(uint4*)(out + at) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
-                    *(uint4*)(out + at + g.N) = make_uint4(du[0], du[1], du[2], du[3]);
                 }
-            } else {
-                for (int e = lane; e < 64 * 128; e += 64) {
-                    const int row = e >> 7, c = e & 127;
-                    if (r0 + row >= g.M || c0 + c >= g.N) continue;
-                    const int64_t at = (r0 + row) * 2 * g.N + c0 + c;
-                    const float gv = __uint_as_float((uint32_t)g.gate_up[at] << 16);
-                    const float uv = __uint_as_float((uint32_t)g.gate_up[at + g.N] << 16);
-                    const float dh = *(const float*)(reg + row * RS + 4 * c);
-                    const ActGrad a = act_grad<ACT>(gv);
-                    out[at] = (uint16_t)bf16x2_rne(dh * uv * a.df, 0.0f);
-                    out[at + g.N] = (uint16_t)bf16x2_rne(dh * a.f, 0.0f);
-                }
+                asm volatile("" ::: "memory");
+            });
+            if (!CHUNKS && left > 0 && left < 8) {   // the lanes whose chunk N ends in
+                for (int r = lane >> 4; r < 64 && 64 * H + r < rows; r += 4)
+                    for (int e = 0; e < (int)left; ++e) {
+                        const int64_t i = i0 + (int64_t)(64 * H + r - (lane >> 4)) * 2 * g.N + e;
+                        const float gv = __uint_as_float((uint32_t)g.gate_up[i] << 16);
+                        const float uv = __uint_as_float((uint32_t)g.gate_up[i + g.N] << 16);
+                        const float dh = *(const float*)(reg + r * RS + 4 * (col + e));
+                        const ActGrad a = act_grad<ACT>(gv);
+                        ((uint16_t*)g.c)[i] = (uint16_t)bf16x2_rne(dh * uv * a.df, 0.0f);
+                        ((uint16_t*)g.c)[i + g.N] = (uint16_t)bf16x2_rne(dh * a.f, 0.0f);
+                    }
             }
             asm volatile("" ::: "memory");
         });
+    };
+    with_act(g.act, [&](auto act_c) {
+        if (chunks) epilogue(act_c, std::true_type{});
+        else epilogue(act_c, std::false_type{});
     });
 }
 
