@@ -1298,4 +1298,206 @@ __device__ __forceinline__ void tile_of32(uint32_t nbm, uint32_t nbn, uint32_t i
     tn = in / rows;
 }
 
+// ---------------------------------------------------------------- persistent NVFP4 kernel
+//
+// K a multiple of 256, at least 512.  At most one workgroup per CU: workgroup b computes the output tiles b, b + P,
+// b + 2P, ... (P = gridDim.x, a multiple of 8 whenever it is below the tile count, so that all
+// tiles of a workgroup have the XCD phase tile_of assumes).  The LDS ring and the operand
+// pipeline of nvw_main_loop run on from one tile to the next: the next tile's slices 0-2 and
+// its first two scale groups are fetched during the current tile's last three slices, and its
+// first MFMA step is read and dequantized during the current tile's last step.  In between,
+// each lane stores its accumulators straight to C (the ring already holds the next tile, so
+// the epilogue cannot stage through LDS) and the next tile starts at once.  With one tile per
+// workgroup, every workgroup of the chip stores its tile at the same moment and then waits for
+// its successor's first slices: at M = 16384, N = 14336 that launch spends about 9 us per tile
+// outside the K loop (a K sweep), 5.7 us of them on the stores (the same kernel with the
+// stores dropped).
+//
+// Between two tiles the output goes out through the one LDS stage that is free at that point,
+// the stage of the tile's last slice (the next tile's slice 3 lands there only after the DMA
+// issued in its slice 0): each wave stages its 128 x 32 TN block in passes through its own
+// 8 KiB of that stage and stores whole 16-byte chunks of rows, so that a store instruction
+// covers whole 128-byte lines of C (storing 4 accumulators per lane straight from registers
+// touches 32 lines per instruction and measured slower).  The stores are buffer stores through
+// a resource over the tile's rows of C, issued by every lane (a chunk outside C gets an offset
+// past the range and is dropped), so a wave issues exactly nvp_stores<OUT_F32>() of them per
+// tile.  The vector-memory counter retires operations in issue order, and the DMAs that the
+// tops of the next tile's slices 0 and 1 wait for were issued before the stores: those two
+// waits allow the stores and the DMAs issued after them in flight, and the stores drain while
+// the two slices run.  Every other wait is the one of nvw_main_loop.
+// The resources that change from tile to tile.
+struct GatedWords {
+    RsrcWords o;
+    u32x4s up;
+};
+__device__ __forceinline__ RsrcWords nvp_words(const MxDma& d) { return d.o; }
+__device__ __forceinline__ GatedWords nvp_words(const GatedDma& d) { return GatedWords{d.o, d.up}; }
+__device__ __forceinline__ void nvp_set(MxDma& d, const RsrcWords& w) { d.o = w; }
+__device__ __forceinline__ void nvp_set(GatedDma& d, const GatedWords& w) {
+    d.o = w.o;
+    d.up = w.up;
+}
+
+__device__ __forceinline__ RsrcWords nvp_rsrc(const GemmArgs& g, int64_t m0, int64_t n0) {
+    const int64_t rb = g.ld / 2, sb = g.ld / 16;
+    const int64_t ra = tile_rows(g.M - m0, GBM), rbn = tile_rows(g.N - n0, GBN);
+    return RsrcWords{rsrc_words(g.a_codes + m0 * rb, ra * rb), rsrc_words(g.b_codes + n0 * rb, rbn * rb),
+                     rsrc_words(g.a_scales + m0 * sb, ra * sb), rsrc_words(g.b_scales + n0 * sb, rbn * sb)};
+}
+
+__device__ __forceinline__ GatedWords nvp_rsrc(const GatedArgs& g, int64_t m0, int64_t n0) {
+    return nvp_words(make_dma<2, 16>(g, m0, n0, (int)(threadIdx.x & 63)));
+}
+
+// Columns of C (of h) in a tile.
+__device__ __forceinline__ constexpr int64_t nvp_tile_n(const GemmArgs&) { return GBN; }
+__device__ __forceinline__ constexpr int64_t nvp_tile_n(const GatedArgs&) { return GBN / 2; }
+
+// An accumulator read where it is used.  The "a" constraint keeps the value in its AGPR up to
+// this point; with plain reads the register allocator copies all 256 accumulators of a tile
+// to VGPRs right after their last MFMAs, and the persistent kernel then spills.
+__device__ __forceinline__ float acc_read(float a) {
+    float v;
+    asm("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
+    return v;
+}
+
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_barrier" ::: "memory"); }
+
+// The tiles blockIdx.x + it P, it < items, of nbm x nbn.  begin(m0) is called at the top of each tile,
+// store(m0, n0, acc, stage) at its end, which issues exactly NST vector-memory operations per lane
+// besides what begin asked for.
+template <int NST, class G, class BEGIN, class STORE>
+__device__ __forceinline__ void nvp_tiles(const G& g, int64_t nbm, int64_t nbn, int64_t P, int items, uint8_t* lds,
+                                          int wm, int wn, int lane, BEGIN&& begin, STORE&& store) {
+    constexpr int TN = 4, NW = 4, DC = 8, DG = 2, PSTEP = 2;
+    const int frow = lane & 31, kh = lane >> 5;
+    const int nk = (int)(g.K / 128);   // even, >= 4
+    auto origin = [&](int it, int64_t& m0, int64_t& n0) {   // tiles < 2^31 (host check)
+        uint32_t tm, tn;
+        tile_of32((uint32_t)nbm, (uint32_t)nbn, blockIdx.x + (uint32_t)it * (uint32_t)P, tm, tn);
+        m0 = (int64_t)tm * GBM;
+        n0 = (int64_t)tn * nvp_tile_n(g);
+    };
+    int64_t m0, n0, m1 = 0, n1 = 0;
+    origin(0, m0, n0);
+    auto d = make_dma<2, 16>(g, m0, n0, lane);
+    auto rc = nvp_words(d), rn = rc;   // resources of the current and of the next tile
+    bool has_next = items > 1;
+    if (has_next) {
+        origin(1, m1, n1);
+        rn = nvp_rsrc(g, m1, n1);
+    }
+    // ring positions by global slice / scale-group index (a tile's slice 0 is slice it * nk)
+    auto buf = [&](int k) { return lds + (k & 3) * NV4_CODES; };
+    auto sbuf = [&](int grp) { return lds + 4 * NV4_CODES + (grp & 1) * NV4_SREC; };
+
+    floatx16 acc[4][TN];   // each tile's first step writes them (nvw_mfma_first)
+
+    // prologue of the first tile, as in nvw_main_loop (nk >= 4: groups 0 and 1 both exist)
+    nv4_dma_group<NW>(d, 0, true, sbuf(0));
+    nv4_dma_group<NW>(d, 1, true, sbuf(1));
+    static_for<0, 3>([&](auto k_c) {
+        constexpr int K0 = decltype(k_c)::value;
+        static_for<0, 4>([&](auto p_c) { nv4_dma_codes<decltype(p_c)::value, NW>(d, 64u * K0, true, buf(K0)); });
+    });
+    nv4_dma_group<NW>(d, 0, false, buf(3));   // no traffic; keeps the wait counts uniform
+    wait_vm_barrier<2 * DC + DG>();
+
+    NvQuadT<TN> q0, q1;
+    NvWordsT<TN> w;
+    NvOpsT<TN> cur, nxt;
+    NvRecT<TN> rec;
+    uint32_t sa[4], sb[TN], san[4], sbn[TN];
+    nvw_read_recs<TN>(sbuf(0), wm, wn, frow, rec);
+    nvw_pick_scales<0, TN>(rec, kh, sa, sb);
+    nvw_read_quad<0, TN>(buf(0), wm, wn, frow, kh, q0);
+    nvw_words_of<0, TN>(q0, w);
+    nvw_ops<0, TN>(w, sa, sb, cur);
+
+    for (int it = 0; it < items; ++it) {
+        const int gs0 = it * nk;
+        begin(m0);
+        // slice kt of this tile; in the tile's last slice (LAST) the last step neither reads nor
+        // dequantizes the next tile's first step: that happens after the stores, so that those
+        // operands are not live across the epilogue
+        auto slice = [&](int kt, auto odd_c, auto last_c, auto first_c) {
+            constexpr bool ODD = decltype(odd_c)::value, LAST = decltype(last_c)::value;
+            constexpr bool FIRST = decltype(first_c)::value;
+            // the previous tile's stores may be in flight at the tops of slices 0 and 1
+            constexpr int W0 = DC + DG + NST < 63 ? DC + DG + NST : 63, W1 = DC + NST < 63 ? DC + NST : 63;
+            if (kt < 2 && it > 0) {
+                if constexpr (ODD) wait_vm_barrier<W1>();
+                else wait_vm_barrier<W0>();
+            } else if constexpr (ODD) wait_vm_barrier<DC>();
+            else wait_vm_barrier<DC + DG>();
+            const int kd = kt + 3;
+            const bool nx = kd >= nk;              // the slice fetched now belongs to the next tile
+            const bool live = !nx || has_next;
+            auto dd = d;
+            nvp_set(dd, nx ? rn : rc);
+            const uint32_t kloc = (uint32_t)(nx ? kd - nk : kd);
+            uint8_t* db = buf(gs0 + kd);
+            const uint8_t* cb = buf(gs0 + kt);
+            const uint8_t* nb = buf(gs0 + kt + 1);
+            static_for<0, 8>([&](auto s_c) {
+                constexpr int S = decltype(s_c)::value;
+                if constexpr (S % PSTEP == 0) nv4_dma_codes<S / PSTEP, NW>(dd, 64u * kloc, live, db);
+                if constexpr (ODD && S == 1) nv4_dma_group<NW>(dd, kloc / 2, live, sbuf((gs0 + kd) / 2));
+                if constexpr (S == 2) nvw_read_quad<1, TN>(cb, wm, wn, frow, kh, q1);
+                if constexpr (S == 6 && !LAST) nvw_read_quad<0, TN>(nb, wm, wn, frow, kh, q0);
+                if constexpr (ODD && S == 5) nvw_read_recs<TN>(sbuf((gs0 + kt + 1) / 2), wm, wn, frow, rec);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (S + 1 < 8) {
+                    if constexpr (S + 1 < 4) nvw_words_of<S + 1, TN>(q0, w);
+                    else nvw_words_of<S + 1, TN>(q1, w);
+                    nvw_ops<S + 1, TN>(w, sa, sb, nxt);
+                } else if constexpr (!LAST) {
+                    nvw_words_of<0, TN>(q0, w);
+                    nvw_pick_scales<ODD ? 0 : 1, TN>(rec, kh, san, sbn);
+                    nvw_ops<0, TN>(w, san, sbn, nxt);
+                }
+                if constexpr (FIRST && S == 0) nvw_mfma_first<TN>(cur, acc);
+                else nvw_mfma<TN>(cur, acc);
+                if constexpr (S + 1 < 8 || !LAST) nvw_interleave<TN>();
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (S + 1 < 8 || !LAST) cur = nxt;
+            });
+            if constexpr (!LAST) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sa[i] = san[i];
+#pragma unroll
+                for (int j = 0; j < TN; ++j) sb[j] = sbn[j];
+            }
+        };
+        using F_ = std::false_type;
+        using T_ = std::true_type;
+        slice(0, F_{}, F_{}, T_{});
+        slice(1, T_{}, F_{}, F_{});
+        for (int kt = 2; kt < nk - 2; kt += 2) {
+            slice(kt, F_{}, F_{}, F_{});
+            slice(kt + 1, T_{}, F_{}, F_{});
+        }
+        slice(nk - 2, F_{}, F_{}, F_{});
+        slice(nk - 1, T_{}, T_{}, F_{});
+        lds_barrier();   // every wave is done with the stage of the last slice
+        store(m0, n0, acc, buf(gs0 + nk - 1));
+        // the next tile's first step (its slice 0 landed before the top of this tile's last
+        // slice, whose step 5 read its first scale records)
+        nvw_read_quad<0, TN>(buf(gs0 + nk), wm, wn, frow, kh, q0);
+        nvw_words_of<0, TN>(q0, w);
+        nvw_pick_scales<0, TN>(rec, kh, sa, sb);
+        nvw_ops<0, TN>(w, sa, sb, cur);
+        m0 = m1;
+        n0 = n1;
+        rc = rn;
+        has_next = it + 2 < items;
+        if (has_next) {
+            origin(it + 2, m1, n1);
+            rn = nvp_rsrc(g, m1, n1);
+        }
+    }
+    wait_vm<0>();   // no DMA may still write this workgroup's LDS when the wave ends
+}
+
 }  // namespace bsq
