@@ -15,7 +15,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbsq.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["quantize.hip", "gemm.hip", "gated.hip", "matvec.hip", "grads.hip", "api.cpp"]
+SOURCES = ["quantize.hip", "gemm.hip", "gated.hip", "gated_small.hip", "matvec.hip", "grads.hip", "api.cpp"]
 
 # Strict IEEE binary32: no FMA contraction, correctly rounded division/sqrt, IEEE
 # denormals.  Packed-fp32 instructions are disabled for the device code.

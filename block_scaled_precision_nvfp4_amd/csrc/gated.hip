@@ -9,32 +9,10 @@
 // output land in the same lane (GatedDma).  h comes from the unrounded fp32 g and u, and dh is never
 // rounded nor stored: the roundings are the fp32 sums, the scale factors, a few fp32 operations of the
 // activation and one bf16 rounding per output.
-#include "activation.hpp"
-#include "gemm_tile.hpp"
+#include "gated.hpp"
 #include "launch.hpp"
 
 namespace bsq {
-
-// Cache policy of a buffer access whose data is not used again soon (non-temporal): gate, up and their gradients
-// leave L2 to the operands (16384 x 14336 x 4096 backward: 1034 -> 989 us).
-constexpr int STREAM = 2;
-
-// Eight bf16 values at any multiple of an element (rows of tensors whose width is no multiple of 8).
-struct __attribute__((packed, aligned(2))) Bf16x8Any { uint32_t w[4]; };
-
-__device__ __forceinline__ u32x4s load_any(const uint16_t* p) {
-    const Bf16x8Any v = *(const Bf16x8Any*)p;
-    return u32x4s{v.w[0], v.w[1], v.w[2], v.w[3]};
-}
-__device__ __forceinline__ void store_any(uint16_t* p, u32x4s v) { *(Bf16x8Any*)p = Bf16x8Any{{v.x, v.y, v.z, v.w}}; }
-
-// Calls body(std::integral_constant<int, ACT>) for the run-time act.
-template <class F>
-__device__ __forceinline__ void with_act(int act, F&& body) {
-    if (act == 0) body(std::integral_constant<int, 0>{});
-    else if (act == 1) body(std::integral_constant<int, 1>{});
-    else body(std::integral_constant<int, 2>{});
-}
 
 // The tile's K loop.  MODE and SL (MXFP8): where scales and codes come from, as in the main loop; each
 // kernel holds one of the loops (several in one function cost it its register allocation).
@@ -248,22 +226,6 @@ __global__ __launch_bounds__(256, 1) void gated_nvp_kernel(GatedArgs g, int64_t 
 
 // ---------------------------------------------------------------- backward
 
-struct GatedBackArgs : GemmArgs {   // c: the gradient of [gate, up], [M][2N] bf16
-    const uint16_t* gate_up;        // [M][2N] bf16
-    int act;
-};
-
-// Both gradients of 8 columns of a row (bf16 pairs) from dh and their gate and up.
-template <int ACT>
-__device__ __forceinline__ void gated_grads(const float (&dh)[8], u32x4s gate, u32x4s up, u32x4s& dg, u32x4s& du) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const ActGrad a = act_grad<ACT>(bf16_lo(gate[e])), b = act_grad<ACT>(bf16_hi(gate[e]));
-        dg[e] = bf16x2_rne(dh[2 * e] * bf16_lo(up[e]) * a.df, dh[2 * e + 1] * bf16_hi(up[e]) * b.df);
-        du[e] = bf16x2_rne(dh[2 * e] * a.f, dh[2 * e + 1] * b.f);
-    }
-}
-
 // One tile per workgroup: 256 x 256 of dh.  Epilogue in two passes of 64 rows per wave: dh goes through the
 // wave's own LDS region in fp32, then each lane takes 8 columns of a row, reads their gate and up (16
 // bytes each) and writes both gradients.  The tile's 512 KiB of gate, up and gradients are a third of the
@@ -413,6 +375,16 @@ static int with_loop(int fmt, int64_t K, int slab, F&& launch) {
     return (int)hipGetLastError();
 }
 
+// Whether 64 x 64 tiles (gated_small.hip) are faster than `tiles` of these.  They fill the chip where these
+// leave it idle, but read their operands 4 times as often and, in MXFP8, feed the MFMA far less well than the
+// large tile's aligned loops.  us large / small, forward NVFP4: 63 / 12 at 16 tiles (333 x 1003 x 2080), 79 / 38
+// at 32 (1024 x 1024 x 4096), 30 / 25 at 64, 34 / 45 at 128; MXFP8: 24 / 7 at 16, 47 / 53 at 32, 28 / 26 at 68
+// with K = 1056, whose large tiles fetch scale bytes one by one.  Backward NVFP4: 88 / 13 at 8, 42 / 33 at 64, 48 / 58
+// at 128; MXFP8: 48 / 29 at 16, 25 / 17 at 32, 27 / 32 at 64.
+static bool use_small(int fmt, int64_t K, int64_t tiles, bool backward) {
+    return tiles <= (fmt == 0 || K % (MX_GROUP * 64) != 0 ? 64 : backward ? 32 : 24);
+}
+
 int64_t gated_tiles(int64_t M, int64_t N) { return ((M + GBM - 1) / GBM) * ((N + GBN / 2 - 1) / (GBN / 2)); }
 
 // Workgroups of a persistent launch, or 0 where it does not apply: per-tensor scales, K a multiple of 256 and at
@@ -442,6 +414,7 @@ int launch_gated_gemm(int fmt, int act, int64_t M, int64_t N, int64_t K, const u
     g.u_s_enc = up_s_enc;
     g.gate_up = (uint16_t*)gate_up;
     g.act = act;
+    if (use_small(fmt, K, gated_tiles(M, N), false)) return launch_gated_small(fmt, g, hip_stream);
     const int64_t p = fmt == 0 ? persistent_workgroups(g) : 0;
     if (p > 0) {
         const auto launch = [&](auto save, auto a) {
@@ -470,6 +443,7 @@ int launch_gated_gemm_backward(int fmt, int act, int64_t M, int64_t N, int64_t K
     g.gate_up = (const uint16_t*)gate_up;
     g.act = act;
     const int64_t tiles = ((M + GBM - 1) / GBM) * ((N + GBN - 1) / GBN);
+    if (use_small(fmt, K, tiles, true)) return launch_gated_backward_small(fmt, g, hip_stream);
     return with_loop(fmt, K, slab, [&](auto f, auto mode, auto sl) {
         hipLaunchKernelGGL((gated_backward_kernel<decltype(f)::value, decltype(mode)::value, decltype(sl)::value>),
                            dim3((unsigned)tiles), dim3(256), 0, (hipStream_t)hip_stream, g);

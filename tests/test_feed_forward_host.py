@@ -128,3 +128,14 @@ def test_plain_derivatives_against_differences(act):
     e = 1e-5
     d = (act64(g + e, act)[0] - act64(g - e, act)[0]) / (2 * e)
     assert float((d - act64(g, act)[1]).abs().max()) < 1e-8
+
+
+def test_clip_in_one_call_refusals(L):
+    def call(**kw):
+        a = dict(p=[FAKE], n=[8], d=[1], m=1.0, norm=FAKE, ws=FAKE)
+        a.update(kw)
+        P, N, D = (C.c_void_p * 1)(*a["p"]), (C.c_int64 * 1)(*a["n"]), (C.c_int * 1)(*a["d"])
+        return L.clip_grad_norm(P, None, N, D, 1, a["m"], a["norm"], a["ws"], None)
+    assert call(m=-1.0) == 3 and call(m=math.nan) == 3 and call(d=[2]) == 3
+    assert call(norm=None) == 1 and call(ws=None) == 1 and call(p=[None]) == 1
+    assert call(norm=FAKE + 1) == 6 and call(ws=FAKE + 8) == 6 and call(p=[FAKE + 2]) == 6

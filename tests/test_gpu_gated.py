@@ -130,6 +130,25 @@ def test_forward_many_tiles(fmt, M, F, K):
     forward(fmt, 2, M, F, K, False, most=96)
 
 
+# just below and above the sizes where the kernels change over from 64 x 64 to 256 x 256 tiles
+@pytest.mark.parametrize("fmt,M,F,K", [(NV, 2048, 1024, 256), (NV, 2049, 1032, 256), (NV, 2049, 1033, 288), (MX, 1536, 512, 512),
+                                       (MX, 1537, 520, 512), (MX, 1537, 517, 512), (MX, 2049, 1033, 544),
+                                       (MX | SLAB, 1537, 520, 512), (MX | bsq.FMT_MX_SLAB_A, 1537, 517, 1024),
+                                       (MX | bsq.FMT_MX_SLAB_B, 1800, 700, 512), (NV | AR | BR, 2049, 1033, 256),
+                                       (NV | BR, 2100, 1041, 96)])
+def test_forward_large_and_small_tiles(fmt, M, F, K):
+    forward(fmt, K % 3, M, F, K, True, most=96)
+
+
+@pytest.mark.parametrize("fmt,M,F,K", [(NV, 2048, 2048, 256), (NV, 2049, 2056, 256), (NV, 2049, 2057, 288), (MX, 2048, 1024, 512),
+                                       (MX, 2049, 1032, 512), (MX, 2049, 1033, 512), (MX, 2049, 2059, 544),
+                                       (MX | SLAB, 2049, 1037, 512), (MX | bsq.FMT_MX_SLAB_A, 2100, 1032, 1024),
+                                       (MX | bsq.FMT_MX_SLAB_B, 2049, 1036, 512), (NV | AR | BR, 2049, 2051, 256),
+                                       (NV | AR, 2100, 2064, 96)])
+def test_backward_large_and_small_tiles(fmt, M, F, K):
+    backward(fmt, F % 3, M, F, K, most=96)
+
+
 def backward(fmt, act, M, F, K, seed=5, most=192, in_place=False, gate_std=1.5):
     note("gated backward fmt=%#x act=%d %d %d %d" % (fmt, act, M, F, K))
     dy = operand(fmt, AR, bsq.FMT_MX_SLAB_A, M, K, 0.01, seed)

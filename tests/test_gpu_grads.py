@@ -160,3 +160,32 @@ def test_python_refusals():
         bsq.clip_grad_norm(g, math.nan)
     with pytest.raises(ValueError):
         bsq.clip_grad_norm(g, 1.0, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+
+
+def test_tables_that_spill_into_more_launches():
+    # 280 tensors to a launch, 176 with outputs; chunks of 8192; every start in a flat bucket
+    sizes = [1 + (i * 7919) % 20000 for i in range(561)]
+    g = make(sizes, "fbf", 21, offset=1)
+    n = norm64(g)
+    check(g, 0.5 * n)
+    check(g, 0.5 * n, in_place=True)
+
+
+def test_clip_in_one_call_and_in_two_agree():
+    g = make([70001, 5, 8192, 333], "fb", 22)
+    a, b = [torch.empty_like(t) for t in g], [torch.empty_like(t) for t in g]
+    na = bsq.clip_grad_norm(g, 0.01, out=a)
+    nb = bsq.grad_clip(g, bsq.grad_sumsq(g), 0.01, out=b)
+    assert torch.equal(na, nb) and all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_outputs_at_another_offset_than_their_gradients():
+    g = make([20011, 9000], "fb", 23)
+    buf = {t.dtype: torch.full((40000,), 5.0, dtype=t.dtype, device=DEV) for t in g}
+    out = [buf[t.dtype][3:3 + t.numel()] for t in g]
+    want = [torch.empty_like(t) for t in g]
+    bsq.clip_grad_norm(g, 0.01, out=out)
+    bsq.clip_grad_norm(g, 0.01, out=want)
+    for t, o, w in zip(g, out, want):
+        assert torch.equal(o, w)
+        assert (buf[t.dtype][:3] == 5.0).all() and (buf[t.dtype][3 + t.numel():] == 5.0).all()

@@ -160,3 +160,30 @@ def test_python_refusals():
         bsq.nvfp4_matvec(torch.empty((2, 67), dtype=torch.bfloat16, device=DEV)[:, :64], c, s, se)
     with pytest.raises(ValueError):
         bsq.nvfp4_matvec(x, c, s, se, out=torch.empty((2, 9), dtype=torch.bfloat16, device=DEV))
+
+
+# the tile of tokens changes with their number and with the rows; K of one block, of a part of a chunk, of many
+# chunks; every way that a row's last 64 elements lie
+@pytest.mark.parametrize("M,N,K", [(1, 40, 32), (70, 33, 48), (2, 40, 80), (4, 100, 8208), (1, 33, 16400), (1, 4099, 1136),
+                                   (5, 2000, 4128), (16, 70, 8272), (20, 7000, 336), (33, 3100, 1104), (64, 3300, 2128),
+                                   (64, 500, 4096), (130, 3100, 528), (3, 9000, 512)])
+def test_every_shape_of_a_launch(M, N, K):
+    check(M, N, K, True, torch.float32, seed=60)
+    check_gated(1, M, (N + 1) // 2, K, seed=61)
+
+
+def test_tokens_far_apart():
+    big = torch.zeros((3, 70, 272), dtype=torch.bfloat16, device=DEV)
+    big[:, -1] = torch.randn((3, 272), generator=torch.Generator().manual_seed(71)).to(torch.bfloat16).to(DEV)
+    w = weights(48, 272, 72)
+    assert torch.equal(bsq.nvfp4_matvec(big[:, -1], *w), bsq.nvfp4_matvec(big[:, -1].contiguous(), *w))
+
+
+def test_one_token_gives_what_a_token_of_several_gives_within_rounding():
+    x, w = tokens(8, 1024, 73), weights(300, 1024, 74)
+    many = bsq.nvfp4_matvec(x, *w, out_dtype=torch.float32).cpu().double()
+    want, S = product(x.cpu().double(), nvfp4_values(*w))
+    for m in range(8):
+        one = bsq.nvfp4_matvec(x[m:m + 1], *w, out_dtype=torch.float32).cpu().double()
+        assert_within(one, want[m:m + 1], sum_error(1024, S[m:m + 1]) + store_error(want[m:m + 1], torch.float32), "one")
+        assert float((one - many[m:m + 1]).abs().max() / S[m].max()) < 2 * (1024 + 3) * 2.0 ** -24
