@@ -102,7 +102,13 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle without the Stream object around it, where this torch has that (1 us less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -581,7 +587,7 @@ def _output(out: Optional[torch.Tensor], shape, dtype, dev) -> torch.Tensor:
 # ---------------------------------------------------------------- gradient clipping
 
 _GRAD_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
-_device_of, _dtype_of = attrgetter("device"), attrgetter("dtype")
+_dtype_of = attrgetter("dtype")
 
 
 def _list_check(tensors: list, name: str, dev):
@@ -622,7 +628,7 @@ class _GradList:
     def _arrays(tensors: list, name: str, dev):
         try:
             kinds = array("i", map(_GRAD_DTYPES.__getitem__, map(_dtype_of, tensors)))
-            good = (dev.type == "cuda" and all(map(dev.__eq__, map(_device_of, tensors)))
+            good = (dev.type == "cuda" and set(map(torch.Tensor.get_device, tensors)) == {dev.index}
                     and all(map(torch.Tensor.is_contiguous, tensors)))
         except (AttributeError, KeyError, TypeError):
             good = False
