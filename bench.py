@@ -63,6 +63,7 @@ def parse():
 
 
 GEMM_SOURCES = ("block_scaled_precision_nvfp4_amd/csrc/gemm.hip",
+                "block_scaled_precision_nvfp4_amd/csrc/gemm_tile.hpp",
                 "block_scaled_precision_nvfp4_amd/csrc/device_common.hpp")
 QUANT_SOURCES = ("block_scaled_precision_nvfp4_amd/csrc/quantize.hip",
                  "block_scaled_precision_nvfp4_amd/csrc/device_common.hpp")

@@ -9,6 +9,12 @@
 // output land in the same lane (GatedDma).  h comes from the unrounded fp32 g and u, and dh is never
 // rounded nor stored: the roundings are the fp32 sums, the scale factors, a few fp32 operations of the
 // activation and one bf16 rounding per output.
+//
+// Measured at 16384 x 14336 x 4096.  Forward, NVFP4, g and u kept: 2.74 - 2.82 ms, 1366 - 1406 TFLOP/s, the rate
+// of the plain NVFP4 GEMM, whose loop (VALU issue of the dequantization) bounds it; the 1.4 GB of output
+// drain behind the next tile's loop.  Backward, MXFP8 in the slab layout: 1.00 ms, of which the K loops take
+// 0.69, the activation's arithmetic 0.08 and the 1.9 GB of gate, up and gradients the rest (each timed by
+// leaving the others out).
 #include "gated.hpp"
 #include "launch.hpp"
 

@@ -17,6 +17,9 @@
 // search and walks on.  The scaling walks each range backwards: what the norm read last is what the
 // caches still hold.  A chunk is read in 16-byte vectors from its first element, wherever that lies:
 // tensors in a flat bucket start at any multiple of their element.
+//
+// 352 M fp32 elements: 800 us, the norm 231 us (6.1 TB/s), the scaling 530 us (5.3 TB/s read and written; a
+// large copy reaches 4.7).  30 thousand elements in 37 tensors: 5 + 6 us of kernels.
 #include "device_common.hpp"
 #include "launch.hpp"
 

@@ -11,6 +11,12 @@
 // significant bits and lies in [2^-10, 2688].  The bf16 MFMA multiplies exactly and accumulates in
 // binary32.  The only roundings are those sums, a block's scale where it is applied to a block's sum, one
 // division by the tensor (or row) scale and the output's.
+//
+// Measured in a graph, weights rotating through 600 MB: one token, 4096 x 14336 9.9 us (3.3 TB/s of weights, a
+// large copy on this card moves 4.7), 16384 x 16384 34.4 us (4.4 TB/s), gated 14336 x 4096 16.5 us (4.0
+// TB/s); 16 tokens, 4096 x 14336 18.1 us, gated 14336 x 4096 24.8 us; 64 tokens, gated 14336 x 8192 63 us. The
+// smallest, 1 x 256 x 256, takes 2.2 us. What is left at these sizes is the way in and out: the launch, the
+// first trip to memory, the join.
 #include "activation.hpp"
 #include "launch.hpp"
 
