@@ -6,7 +6,8 @@
  * Philox-keyed stochastic rounding, optional 16-point random Hadamard transform),
  * NVFP4 dequantization, the MXFP8 cast, the standalone Hadamard transform, and the
  * block-scaled GEMM C = A * B^T that consumes the quantized operands with fp32
- * accumulation.
+ * accumulation; around them the products of a gated feed-forward block with their backward
+ * pass, products of a few bf16 tokens with NVFP4 weights, and gradient clipping.
  *
  * Conventions shared by every entry point:
  *   - Tensors are row-major and contiguous.  A bf16 tensor x has shape [rows][cols].
@@ -419,8 +420,9 @@ int nvfp4_linear_backward(const void* dy, const void* w, const void* saved, int6
 /*
  * nvfp4_matvec -- y[M][N] = x[M][K] W[N][K]^T for a few tokens x in bf16 and NVFP4 weights: the
  * linear layer of a model that serves single tokens from its quantized weights.  The
- * activations are not quantized; every weight code * scale enters exactly, products are
- * summed in fp32 and divided by S once.
+ * activations are not quantized and every weight enters exactly; products are summed in fp32
+ * and divided by S once.  (For M = 1 a block's sum over its codes takes the block scale once,
+ * one rounding more; so a token may differ in the last bits between M = 1 and M > 1.)
  *   flags   0, or BSQ_FMT_B_ROWSCALED: w_s_enc is float[N] (nvfp4_quantize_rowscaled), else float[1].
  *   x       bf16, row m at x + m * ldx elements; ldx >= K, ldx % 8 == 0.
  *   w_codes [N][K/2], w_scales [N][K/16]: rowwise NVFP4 as nvfp4_quantize writes it.  K % 16 == 0.
