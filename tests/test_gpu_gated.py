@@ -308,3 +308,36 @@ def test_python_refusals():
         bsq.blockscaled_gated_gemm_backward(NV, 0, *a, *wg, torch.empty((M, 2 * F), device=DEV))
     with pytest.raises(ValueError):
         bsq.blockscaled_gated_gemm_backward(NV, 0, *a, *other_k, torch.empty((M, 2 * F), dtype=torch.bfloat16, device=DEV))
+
+
+# outputs past 2^31 elements: 76800 x 2 * 14336
+@pytest.mark.parametrize("fmt,K", [(NV, 512), (NV, 96), (MX, 96)])
+def test_outputs_past_2_to_the_31_elements(fmt, K):
+    M, F = 76800, 14336
+    a, wg, wu = (operand(fmt, 0, 0, r, K, std, s) for r, std, s in ((M, 1.0, 1), (F, 2.0 / K ** 0.5, 2), (F, 1.0 / K ** 0.5, 3)))
+    h, gu = bsq.blockscaled_gated_gemm(fmt, 0, *a, *wg, *wu, save_gate_up=True)
+    rows = torch.tensor([0, 255, 256, 37449, 37450, 74898, 74899, M - 257, M - 2, M - 1])   # 37449 * 2F < 2^30 < 37450 * 2F
+    cols = torch.tensor([0, 127, 128, F - 129, F - 1])
+    part = tuple(t[rows.to(DEV)] if t is not None and t.dim() == 2 else t for t in a)
+    every = torch.arange(len(rows))
+    g, eg = product64(fmt, part, wg, False, False, every, cols)
+    u, eu = product64(fmt, part, wu, False, False, every, cols)
+    f, _ = act64(g, 0)
+    want = f * u
+    e = 1.13 * eg * (u.abs() + eu) + f.abs() * eu + want.abs() * (act_rel(g.abs() + eg, 0) + 2 * F32)
+    at = lambda t: t[rows.to(DEV)][:, cols.to(DEV)].cpu()   # noqa: E731
+    assert_within(at(h), want, rounded(want, e), "h")
+    assert_within(at(gu[:, :F]), g, rounded(g, eg), "gate")
+    assert_within(at(gu[:, F:]), u, rounded(u, eu), "up")
+    keep = gu[rows.to(DEV)].cpu()
+    dy, w = operand(fmt, 0, 0, M, K, 0.01, 4), operand(fmt, 0, 0, F, K, 0.02, 5)
+    d = bsq.blockscaled_gated_gemm_backward(fmt, 0, *dy, *w, gu, out=gu)
+    part = tuple(t[rows.to(DEV)] if t is not None and t.dim() == 2 else t for t in dy)
+    dh, e = product64(fmt, part, w, False, False, every, cols)
+    g, u = keep[:, :F][:, cols].double(), keep[:, F:][:, cols].double()
+    f, df = act64(g, 0)
+    rel = act_rel(g, 0) + 4 * F32
+    eg = e * (u * df).abs() + (dh.abs() + e) * u.abs() * act_grad_terms(g, 0) * rel
+    eu = e * f.abs() + (dh.abs() + e) * f.abs() * rel
+    assert_within(at(d[:, :F]), dh * u * df, rounded(dh * u * df, eg), "d_gate")
+    assert_within(at(d[:, F:]), dh * f, rounded(dh * f, eu), "d_up")

@@ -189,3 +189,15 @@ def test_outputs_at_another_offset_than_their_gradients():
     for t, o, w in zip(g, out, want):
         assert torch.equal(o, w)
         assert (buf[t.dtype][:3] == 5.0).all() and (buf[t.dtype][3 + t.numel():] == 5.0).all()
+
+
+def test_a_tensor_past_2_to_the_31_elements():
+    n = (1 << 31) + 4099
+    g = torch.full((n,), 0.5, dtype=torch.bfloat16, device=DEV)
+    g[-1] = 2.0
+    norm = bsq.clip_grad_norm([g], 1.0)
+    want = math.sqrt(0.25 * (n - 1) + 4.0)
+    assert abs(float(norm) - want) <= want * 2.0 ** -23
+    c = 1.0 / (want + 1e-6)
+    for i, v in ((0, 0.5), (1 << 30, 0.5), ((1 << 31) - 1, 0.5), (1 << 31, 0.5), (n - 2, 0.5), (n - 1, 2.0)):
+        assert abs(float(g[i]) - v * c) <= v * c * (2.0 ** -8 + 2.0 ** -20), i

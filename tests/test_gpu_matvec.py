@@ -187,3 +187,17 @@ def test_one_token_gives_what_a_token_of_several_gives_within_rounding():
         one = bsq.nvfp4_matvec(x[m:m + 1], *w, out_dtype=torch.float32).cpu().double()
         assert_within(one, want[m:m + 1], sum_error(1024, S[m:m + 1]) + store_error(want[m:m + 1], torch.float32), "one")
         assert float((one - many[m:m + 1]).abs().max() / S[m].max()) < 2 * (1024 + 3) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("M", [1, 3])
+def test_weights_past_2_to_the_32_bytes(M):
+    N, K = 530000, 16400   # 4.3 GB of codes, rows of neither 16 nor 64 bytes
+    g = torch.Generator(device=DEV).manual_seed(80)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8, device=DEV)
+    scales = torch.randint(0, 127, (N, K // 16), generator=g, dtype=torch.uint8, device=DEV)
+    s = torch.rand(N, generator=g, device=DEV) * 900 + 100
+    x = tokens(M, K, 81)
+    y = bsq.nvfp4_matvec(x, codes, scales, s, out_dtype=torch.float32)
+    rows = torch.tensor([0, 15, 16, 261870, 261888, 523760, 523776, N - 17, N - 1], device=DEV)
+    want, S = product(x.cpu().double(), nvfp4_values(codes[rows], scales[rows], s[rows]))
+    assert_within(y[:, rows], want, sum_error(K, S) + store_error(want, torch.float32), "y")
