@@ -125,12 +125,20 @@ struct MxFrag {
 // aligned-record conditions.  MX_GSLAB is the K-grouped launch with slab operands: a group's
 // K range starts at any multiple of 32, so its scales take offset records and its codes are
 // addressed from the whole band (mx_gslab_codes).
-constexpr int MX_SLOTS = 0, MX_RECS = 1, MX_OFFRECS = 2, MX_SLAB = 3, MX_GSLAB = 4;
+//  - dword records (MX_DRECS; any K, base 16-byte aligned; the gated products): the scale bytes
+//    of 4 slices of a row are 8, which the 3 aligned dwords from the one that holds the first
+//    cover, fetched every 4 slices as NVFP4's per-slice records are (nvs_dma_recs), into
+//    [group parity][operand][256 rows][12 B] after the code stages.  6 DMAs per lane for 4 slices
+//    where byte slots take 16.
+constexpr int MX_SLOTS = 0, MX_RECS = 1, MX_OFFRECS = 2, MX_SLAB = 3, MX_GSLAB = 4, MX_DRECS = 5;
+constexpr int MX_DGROUP = 4;                               // slices per dword record
+constexpr int MX_DREC = 2 * GBM * 12;                      // 6 KiB per group
 constexpr int MX_CODES = 2 * GBM * ROWB;                  // 32 KiB
 constexpr int MX_STAGE_SLOTS = MX_CODES + 2 * GBM * 2 * 4;  // 36 KiB
 constexpr int MX_GROUP = 8;                                // slices per grouped scale record
 constexpr int MX_SREC = 2 * GBM * 16;                      // 8 KiB per scale group
-static_assert(4 * MX_STAGE_SLOTS <= Fmt<1>::LDS && 4 * MX_CODES + 3 * MX_SREC <= Fmt<1>::LDS, "MXFP8 LDS");
+static_assert(4 * MX_STAGE_SLOTS <= Fmt<1>::LDS && 4 * MX_CODES + 3 * MX_SREC <= Fmt<1>::LDS &&
+                  2 * MX_DREC <= 3 * MX_SREC, "MXFP8 LDS");
 
 // LDS DMA: a buffer load whose data goes straight to LDS.  A wave-wide DMA writes 64
 // consecutive LDS slots starting at the wave-uniform address in M0 -- 16 bytes per lane for
@@ -232,17 +240,15 @@ __device__ __forceinline__ void mx_dma_codes(const D& d, int64_t b0, bool live, 
 }
 
 // MXFP8 per-slice scale slots of the slice starting at element k0.
-template <int P, class D>
-__device__ __forceinline__ void mx_dma_slots(const D& d, int64_t k0, bool live, uint8_t* buf) {
+template <int P>
+__device__ __forceinline__ void mx_dma_slots(const MxDma& d, int64_t k0, bool live, uint8_t* buf) {
     const int s0 = 256 * P + 64 * d.wave;
     const int sl = s0 + d.lane, r = sl >> 1, kb = sl & 1;
     const int64_t kb0 = k0 / 32;
-    const bool in = live && kb0 + kb < (int64_t)d.kblocks;
-    const uint32_t off = in ? (uint32_t)r * d.sstride + kb : OOB;
-    const uint32_t offb = in ? (uint32_t)b_slot_row(d, r) * d.sstride + kb : OOB;
+    const uint32_t off = (live && kb0 + kb < (int64_t)d.kblocks) ? (uint32_t)r * d.sstride + kb : OOB;
     const uint32_t soff = live ? (uint32_t)kb0 : 0u;
     dma_u8(d.o.as, lds_addr(buf + MX_CODES + 4 * s0), off, soff);
-    dma_u8(d.o.bs, lds_addr(buf + MX_CODES + 8 * GBM + 4 * s0), offb, soff);
+    dma_u8(d.o.bs, lds_addr(buf + MX_CODES + 8 * GBM + 4 * s0), off, soff);
 }
 
 // The same DMAs where K is a multiple of the slice group (the NVFP4 kernel: K % 256 == 0; the
@@ -436,6 +442,9 @@ __device__ __forceinline__ void mx_read_part(const uint8_t* buf, const uint8_t* 
     } else if constexpr (MODE == MX_OFFRECS || MODE == MX_GSLAB) {
         f.as[P] = sp.a[512 * P];
         f.bs[P] = sp.b[512 * P];
+    } else if constexpr (MODE == MX_DRECS) {
+        f.as[P] = sp.a[32 * 12 * P];
+        f.bs[P] = sp.b[32 * 12 * P];
     } else {
         const uint32_t* slots = (const uint32_t*)(buf + MX_CODES);
         f.as[P] = slots[2 * ra + kh];
@@ -463,6 +472,90 @@ __device__ __forceinline__ void mx_mfma_row(const MxFrag& f, floatx16 (&acc)[4][
                                                                      (int)f.as[P]);
 }
 
+// Scale records of 12 bytes (3 dwords) per row, for NVFP4 per slice and MXFP8 per 4 slices: 8 scale bytes of a
+// row, which start 0 to 3 bytes into the first dword.
+constexpr int NVS_REC = 12;
+constexpr int NVS_DS = 6;   // record DMAs per lane
+static_assert(NVS_DS * 64 * 4 == 2 * GBM * 3, "the records of a slice: 4 waves x 6 DMAs of 64 dwords");
+
+__device__ __forceinline__ void dma_b32(const u32x4s& rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 :: "s"(lds), "v"(voff), "s"(rsrc), "s"(soff) : "m0");
+}
+
+// The resource of record DMA i (0..2) of B: a gated tile's wave takes gate's or up's records per DMA.
+struct GatedRecs {
+    u32x4s r[3];
+};
+__device__ __forceinline__ const u32x4s& b_recs(const u32x4s& r, int) { return r; }
+__device__ __forceinline__ const u32x4s& b_recs(const GatedRecs& r, int i) { return r.r[i]; }
+
+// Record DMAs I0 .. I1-1 (of 6) of the slice whose scale bytes start 8k into each row: DMA i
+// of wave w fills dword slots 64 (w + 4i) .. +64 of the slice's records (A's 768, then B's).
+template <int I0, int I1, class B>
+__device__ __forceinline__ void nvs_dma_recs(const u32x4s& rsa, const B& rsb, const uint32_t (&so)[NVS_DS],
+                                             uint32_t k8, bool live, uint8_t* rec, int wave) {
+#pragma unroll
+    for (int i = I0; i < I1; ++i) {
+        const u32x4s& rs = i >= 3 ? b_recs(rsb, i - 3) : rsa;   // slot groups w + 4i >= 12 belong to B
+        dma_b32(sized(rs, live), lds_addr(rec + 256 * (wave + 4 * i)), so[i] + k8, 0u);
+    }
+}
+
+// B's record resources from the aligned dword below its first scale byte to its last row's, dl bytes
+// into the first dword.
+template <int BLK>
+__device__ __forceinline__ u32x4s nvs_b_recs(const GemmArgs& g, int64_t n0, uint32_t dl, int64_t rows, uint32_t kscale,
+                                             int) {
+    const int64_t sbs = g.ld / BLK;
+    return rsrc_words(g.b_scales + n0 * sbs - dl, (dl + (rows - 1) * sbs + kscale + 3) & ~(int64_t)3);
+}
+
+// A gated tile's: the 12 slot groups of 64 dwords (21 1/3 rows) of B's 256 records are three to 64 rows,
+// gate, up, gate, up, so DMA i of wave w, slot group w + 4i, lies in rows of one of the weights.
+template <int BLK>
+__device__ __forceinline__ GatedRecs nvs_b_recs(const GatedArgs& g, int64_t n0, uint32_t dl, int64_t rows,
+                                                uint32_t kscale, int wave) {
+    const int64_t sbs = g.ld / BLK;
+    GatedRecs q;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const uint8_t* p = ((wave + 4 * i) / 3 & 1) ? g.u_scales : g.b_scales;
+        q.r[i] = rsrc_words(p + n0 * sbs - dl, (dl + (rows - 1) * sbs + kscale + 3) & ~(int64_t)3);
+    }
+    return q;
+}
+
+// Rows of each weight in a tile.
+__device__ __forceinline__ int64_t b_tile_rows(const GemmArgs& g, int64_t n0) { return tile_rows(g.N - n0, GBN); }
+__device__ __forceinline__ int64_t b_tile_rows(const GatedArgs& g, int64_t n0) { return tile_rows(g.N - n0, GBN / 2); }
+
+// MXFP8 dword records of a tile: the resources and the lane's offsets for group 0.
+template <class B>
+struct MxDrecs {
+    u32x4s a;
+    B b;
+    uint32_t so[NVS_DS];
+};
+
+template <class G, class D>
+__device__ __forceinline__ auto mx_drecs(const G& g, const D& d, int64_t m0, int64_t n0) {
+    const int64_t sb = g.ld / 32, ra = tile_rows(g.M - m0, GBM), rbn = b_tile_rows(g, n0);
+    // tile rows are multiples of 4 (128), so a tile's first scale byte is dword-aligned like the tensor
+    auto b = nvs_b_recs<32>(g, n0, 0u, rbn, d.kblocks, d.wave);
+    MxDrecs<decltype(b)> q;
+    q.a = rsrc_words(g.a_scales + m0 * sb, ((ra - 1) * sb + d.kblocks + 3) & ~(int64_t)3);
+    q.b = b;
+#pragma unroll
+    for (int i = 0; i < NVS_DS; ++i) {
+        const bool opb = i >= 3;
+        const int s = 64 * (d.wave + 4 * i - (opb ? 12 : 0)) + d.lane, rt = s / 3, dw = s - 3 * rt;
+        const int r = opb ? b_slot_row(d, rt) : rt;
+        q.so[i] = r < (opb ? rbn : ra) ? (uint32_t)(((uint64_t)r * (uint64_t)sb) & ~(uint64_t)3) + 4u * dw : OOB;
+    }
+    return q;
+}
+
 // MXFP8 main loop over K slices with 4 LDS code stages.  At the top of slice kt each wave
 // waits for its own DMAs of slice kt+1 (issued two slices earlier; only those issued during
 // slice kt-1 may still be in flight), then a barrier publishes slice kt+1 to the workgroup
@@ -483,6 +576,10 @@ struct MxLds {
     static __device__ __forceinline__ uint8_t* buf(uint8_t* lds, int64_t k) { return lds + (int)(k & 3) * STRIDE; }
     static __device__ __forceinline__ uint8_t* sbuf(uint8_t* lds, int64_t grp) {
         return lds + 4 * MX_CODES + (int)(grp & 1) * MX_SREC;
+    }
+    // dword records of group grp
+    static __device__ __forceinline__ uint8_t* dbuf(uint8_t* lds, int64_t grp) {
+        return lds + 4 * MX_CODES + (int)(grp & 1) * MX_DREC;
     }
     // offset record j, j3 = j mod 3
     static __device__ __forceinline__ uint8_t* rbuf(uint8_t* lds, int j3) { return lds + 4 * MX_CODES + j3 * MX_SREC; }
@@ -520,14 +617,9 @@ __device__ __forceinline__ void mx_scale_rsrc(const GemmArgs& g, int64_t m0, int
     }
 }
 
-// The same of a gated tile, whose scales come as aligned records (make_dma) or per slice: a wave's slots
-// (32 rows of the tile) are all gate's or all up's.
+// A gated tile's scales come as aligned records, which make_dma has, or dword records (MxDrecs).
 template <int MODE>
-__device__ __forceinline__ void mx_scale_rsrc(const GatedArgs& g, int64_t, int64_t n0, MxPlan<GatedDma>& p) {
-    if constexpr (MODE == MX_SLOTS)
-        p.d.o.bs = rsrc_words((p.d.wave & 2 ? g.u_scales : g.b_scales) + n0 * p.d.sstride,
-                              tile_rows(g.N - n0, GBN / 2) * p.d.sstride);
-}
+__device__ __forceinline__ void mx_scale_rsrc(const GatedArgs&, int64_t, int64_t, MxPlan<GatedDma>&) {}
 
 template <int MODE, class G>
 __device__ __forceinline__ auto mx_plan(const G& g, int64_t m0, int64_t n0, int64_t nk, int lane) {
@@ -586,7 +678,8 @@ __device__ __forceinline__ void mx_main_loop(const G& g, int64_t m0, int64_t n0,
     constexpr bool OFFR = MODE == MX_OFFRECS || MODE == MX_GSLAB;  // offset records
     constexpr int DC = 8;                    // code DMAs per slice per lane
     constexpr int DS = REC ? 0 : 4;          // per-slice scale DMAs
-    constexpr int DG = 2;                    // scale-record DMAs (every MX_GROUP slices)
+    constexpr bool DREC = MODE == MX_DRECS;
+    constexpr int DG = DREC ? NVS_DS : 2;    // scale-record DMAs (every MX_GROUP or MX_DGROUP slices)
     if (nk <= 0) return;
     const auto pl = mx_plan<MODE>(g, m0, n0, nk, lane);
     const auto& d = pl.d;
@@ -599,7 +692,7 @@ __device__ __forceinline__ void mx_main_loop(const G& g, int64_t m0, int64_t n0,
     // scale is NaN.
     const bool hi = lane >= 32;
     const int lrow_a = (wm + (lane & 31)) * 16, lrow_b = GBM * 16 + (wn + (lane & 31)) * 16;
-    const int last_odd = (OFFR && (kbl & 1)) ? nk32 - 1 : -1;
+    const int last_odd = ((OFFR || DREC) && (kbl & 1)) ? nk32 - 1 : -1;
     auto rec_ptrs = [&](int c3, int q, int64_t k) {
         const uint8_t* cur = L::rbuf(lds, c3);
         const uint8_t* nxt = L::rbuf(lds, c3 == 2 ? 0 : c3 + 1);
@@ -611,12 +704,32 @@ __device__ __forceinline__ void mx_main_loop(const G& g, int64_t m0, int64_t n0,
         return sp;
     };
     int g3 = 0;   // offset records: the current group's index mod 3
+    // dword records: the lane's byte of slice k, in the records of its group; a row's bytes start (row sb) mod 4
+    // into its record, and rows 32 apart alike.  A slice past the last one (zero codes) takes the last one's
+    // scales: the bytes in its place are another row's, where a NaN would leak into the sums.
+    [[maybe_unused]] const uint32_t drow = (uint32_t)(lane & 31) * 12u + (((uint32_t)(lane & 31) * d.sstride) & 3u);
+    [[maybe_unused]] auto drec_ptrs = [&](int k) {
+        k = k < nk32 ? k : nk32 - 1;
+        const uint8_t* cur = L::dbuf(lds, k / MX_DGROUP) + drow + 2 * (k & (MX_DGROUP - 1)) + (hi && k != last_odd ? 1 : 0);
+        return MxSPtr{cur + wm * 12, cur + GBM * 12 + wn * 12};
+    };
+    [[maybe_unused]] auto drecs = [&] {
+        if constexpr (DREC) return mx_drecs(g, d, m0, n0);
+        else return 0;
+    }();
+    [[maybe_unused]] auto dma_drecs = [&](int grp) {
+        if constexpr (DREC)
+            nvs_dma_recs<0, NVS_DS>(drecs.a, drecs.b, drecs.so, 8u * (uint32_t)grp, MX_DGROUP * grp < nk32, L::dbuf(lds, grp),
+                                    d.wave);
+    };
 
+    if constexpr (DREC) dma_drecs(0);
     mx_prologue<MODE, SL>(pl, lds);
     wait_vm_barrier<2 * (DC + DS)>();
     MxFrag f0, f1;
     MxSPtr sp0{nullptr, nullptr};
     if constexpr (OFFR) sp0 = rec_ptrs(0, 0, 0);
+    if constexpr (DREC) sp0 = drec_ptrs(0);
     mx_read<MODE>(L::buf(lds, 0), L::sbuf(lds, 0), 0, sp0, wm, wn, lane, f0);
 
     // One slice.  Grouped records: Q = kt mod MX_GROUP (the loop is unrolled by MX_GROUP).
@@ -628,6 +741,9 @@ __device__ __forceinline__ void mx_main_loop(const G& g, int64_t m0, int64_t n0,
         [[maybe_unused]] const int g3n = g3 == 2 ? 0 : g3 + 1;
         if constexpr (OFFR) {
             if (qr == 2) wait_vm_barrier<DC + DG>();   // slice kt-1 also issued a record
+            else wait_vm_barrier<DC>();
+        } else if constexpr (DREC) {
+            if ((kt & (MX_DGROUP - 1)) == 2) wait_vm_barrier<DC + DG>();
             else wait_vm_barrier<DC>();
         } else if constexpr (REC && Q == 2) {
             wait_vm_barrier<DC + DG>();
@@ -643,6 +759,7 @@ __device__ __forceinline__ void mx_main_loop(const G& g, int64_t m0, int64_t n0,
         const int qn = REC ? (Q + 1) % MX_GROUP : 0;
         MxSPtr spn{nullptr, nullptr};
         if constexpr (OFFR) spn = rec_ptrs(qr == MX_GROUP - 1 ? g3n : g3, (qr + 1) & (MX_GROUP - 1), kn);
+        if constexpr (DREC) spn = drec_ptrs((int)kn);
         static_for<0, 4>([&](auto p_c) {
             constexpr int P = decltype(p_c)::value;
             mx_dma_part<MODE, SL, P>(d, kd, live, db);
@@ -656,6 +773,9 @@ __device__ __forceinline__ void mx_main_loop(const G& g, int64_t m0, int64_t n0,
                     const int j = (int)(kt / MX_GROUP) + 2;
                     mx_dma_offrec(d, pl.offa, pl.offb, (uint32_t)j, 16 * j < 15 + kbl, L::rbuf(lds, g3 == 0 ? 2 : g3 - 1));
                 }
+            }
+            if constexpr (DREC && P == 0) {
+                if ((kt & (MX_DGROUP - 1)) == 1) dma_drecs((int)(kt / MX_DGROUP) + 1);
             }
             mx_mfma_row<P>(fc, acc);
             // the reads after the last slice touch a stale (in-bounds) buffer and go unused
@@ -955,16 +1075,9 @@ __device__ __forceinline__ void nvw_main_loop(const G& g, int64_t m0, int64_t n0
 // the code DMAs check each 16-byte chunk (K % 32 == 0: a chunk lies entirely inside or
 // outside K) and the scale bytes past K are cleared, so that nothing beyond the operands' K
 // reaches the sums.
-constexpr int NVS_REC = 12;
 constexpr int NVS_STAGE = NV4_CODES + 2 * GBM * NVS_REC;   // 38 KiB
-constexpr int NVS_DS = 6;                                  // record DMAs per lane per slice
 static_assert(4 * NVS_STAGE <= Fmt<3>::LDS, "NVFP4 per-slice scale LDS");
 static_assert(NVS_DS * 64 * 4 == 2 * GBM * 3, "the records of a slice: 4 waves x 6 DMAs of 64 dwords");
-
-__device__ __forceinline__ void dma_b32(const u32x4s& rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
-    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                 :: "s"(lds), "v"(voff), "s"(rsrc), "s"(soff) : "m0");
-}
 
 // Code DMAs of part P of the slice whose first code byte per row is b0; in the slice that K
 // ends inside (tail, uniform) every lane checks its chunk and carries the whole offset in the
@@ -986,25 +1099,6 @@ __device__ __forceinline__ void nvs_dma_codes(const D& d, uint32_t b0, bool live
     dma_b128(sized(b_codes<P>(d), live), lds_addr(buf + GBM * ROWB + r0 * ROWB), offb, soff);
 }
 
-// The resource of record DMA i (0..2) of B: a gated tile's wave takes gate's or up's records per DMA.
-struct GatedRecs {
-    u32x4s r[3];
-};
-__device__ __forceinline__ const u32x4s& b_recs(const u32x4s& r, int) { return r; }
-__device__ __forceinline__ const u32x4s& b_recs(const GatedRecs& r, int i) { return r.r[i]; }
-
-// Record DMAs I0 .. I1-1 (of 6) of the slice whose scale bytes start 8k into each row: DMA i
-// of wave w fills dword slots 64 (w + 4i) .. +64 of the slice's records (A's 768, then B's).
-template <int I0, int I1, class B>
-__device__ __forceinline__ void nvs_dma_recs(const u32x4s& rsa, const B& rsb, const uint32_t (&so)[NVS_DS],
-                                             uint32_t k8, bool live, uint8_t* rec, int wave) {
-#pragma unroll
-    for (int i = I0; i < I1; ++i) {
-        const u32x4s& rs = i >= 3 ? b_recs(rsb, i - 3) : rsa;   // slot groups w + 4i >= 12 belong to B
-        dma_b32(sized(rs, live), lds_addr(rec + 256 * (wave + 4 * i)), so[i] + k8, 0u);
-    }
-}
-
 // The lane's 4 scale bytes (blocks 4kh .. 4kh+3) of each of its fragments from a slice's
 // records: two dwords at the record's dword oq (0 or 1), shifted right by sh bits (0 or 16,
 // or 8 / 24 for a scale tensor that is not even-aligned), then masked (the bytes past K).
@@ -1023,32 +1117,6 @@ __device__ __forceinline__ void nvs_read_scales(const uint8_t* rec, int wm, int 
         sb[j] = __builtin_amdgcn_alignbit(p[1], p[0], shb) & mask;
     }
 }
-
-// B's record resources from the aligned dword below its first scale byte to its last row's, dl bytes
-// into the first dword.
-__device__ __forceinline__ u32x4s nvs_b_recs(const GemmArgs& g, int64_t n0, uint32_t dl, int64_t rows, uint32_t kscale,
-                                             int) {
-    const int64_t sbs = g.ld / 16;
-    return rsrc_words(g.b_scales + n0 * sbs - dl, (dl + (rows - 1) * sbs + kscale + 3) & ~(int64_t)3);
-}
-
-// A gated tile's: the 12 slot groups of 64 dwords (21 1/3 rows) of B's 256 records are three to 64 rows,
-// gate, up, gate, up, so DMA i of wave w, slot group w + 4i, lies in rows of one of the weights.
-__device__ __forceinline__ GatedRecs nvs_b_recs(const GatedArgs& g, int64_t n0, uint32_t dl, int64_t rows,
-                                                uint32_t kscale, int wave) {
-    const int64_t sbs = g.ld / 16;
-    GatedRecs q;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        const uint8_t* p = ((wave + 4 * i) / 3 & 1) ? g.u_scales : g.b_scales;
-        q.r[i] = rsrc_words(p + n0 * sbs - dl, (dl + (rows - 1) * sbs + kscale + 3) & ~(int64_t)3);
-    }
-    return q;
-}
-
-// Rows of each weight in a tile.
-__device__ __forceinline__ int64_t b_tile_rows(const GemmArgs& g, int64_t n0) { return tile_rows(g.N - n0, GBN); }
-__device__ __forceinline__ int64_t b_tile_rows(const GatedArgs& g, int64_t n0) { return tile_rows(g.N - n0, GBN / 2); }
 
 template <int TN, class G>
 __device__ __forceinline__ void nvs_main_loop(const G& g, int64_t m0, int64_t n0, int64_t nk, uint8_t* lds,
@@ -1072,7 +1140,7 @@ __device__ __forceinline__ void nvs_main_loop(const G& g, int64_t m0, int64_t n0
     const uint8_t* pb = g.b_scales + n0 * sbs;
     const uint32_t dla = (uint32_t)((uintptr_t)pa & 3), dlb = (uint32_t)((uintptr_t)pb & 3);
     const u32x4s rsa = rsrc_words(pa - dla, (dla + (ra - 1) * sbs + kscale + 3) & ~(int64_t)3);
-    const auto rsb = nvs_b_recs(g, n0, dlb, rbn, kscale, d.wave);
+    const auto rsb = nvs_b_recs<16>(g, n0, dlb, rbn, kscale, d.wave);
     uint32_t so[NVS_DS];   // the lane's record DMA offsets for slice 0
 #pragma unroll
     for (int i = 0; i < NVS_DS; ++i) {

@@ -244,9 +244,8 @@ def test_non_finite_values_stay_in_their_row_and_column():
         h = bsq.blockscaled_gated_gemm(fmt, 0, *a, *wg, *wu).cpu()
         bad = torch.zeros((M, F), dtype=torch.bool)
         bad[3], bad[:, 5], bad[:, 7] = True, True, True
-        # a zero code times an invalid scale may stay zero in MXFP8 hardware; NVFP4 gives NaN
         assert torch.equal(h[~bad], clean[~bad])
-        if fmt == MX:
+        if fmt == MX:   # the NVFP4 products take the scale code without a value, which no cast writes, as 480
             assert torch.isnan(h[bad]).all()
     g = torch.tensor([[math.inf, -math.inf, math.nan, 0.0] + [1.0] * 4], dtype=torch.bfloat16, device=DEV)
     u = torch.ones((1, 8), dtype=torch.bfloat16, device=DEV)
@@ -341,3 +340,32 @@ def test_outputs_past_2_to_the_31_elements(fmt, K):
     eu = e * f.abs() + (dh.abs() + e) * f.abs() * rel
     assert_within(at(d[:, :F]), dh * u * df, rounded(dh * u * df, eg), "d_gate")
     assert_within(at(d[:, F:]), dh * f, rounded(dh * f, eu), "d_up")
+
+
+# K-blocks even and odd, slices even and odd, K ending inside a slice; the sizes take the large tiles
+@pytest.mark.parametrize("fmt,K", [(NV, 512), (NV, 544), (NV, 96), (MX, 512), (MX, 544), (MX, 576), (MX, 608), (MX, 160)])
+def test_non_finite_scales_stay_in_their_row_and_column_of_large_tiles(fmt, K):
+    M, F = 2310, 2057
+    a, wg, wu = (operand(fmt, 0, 0, r, K, 0.5, s) for r, s in ((M, 1), (F, 2), (F, 3)))
+    dy, w, gu = operand(fmt, 0, 0, M, K, 0.5, 4), operand(fmt, 0, 0, F, K, 0.5, 5), gauss(M, 2 * F, 1.0, 6)
+    run = lambda: (bsq.blockscaled_gated_gemm(fmt, 0, *a, *wg, *wu).cpu(),   # noqa: E731
+                   bsq.blockscaled_gated_gemm_backward(fmt, 0, *dy, *w, gu).cpu())
+    h0, d0 = run()
+    nan = 0x7F if fmt == NV else 0xFF
+    last = a[1].shape[1] - 1
+    for t in (a, dy):
+        t[1][3, 0] = t[1][259, 1] = t[1][2305, last] = nan
+    wg[1][5, 0] = wg[1][200, last] = wu[1][7, 1] = wu[1][1030, 0] = nan
+    w[1][5, 0] = w[1][200, last] = w[1][1030, 1] = nan
+    h, d = run()
+    rows, cols, wcols = [3, 259, 2305], [5, 200, 7, 1030], [5, 200, 1030]
+    keep = torch.ones((M, F), dtype=torch.bool)
+    keep[rows] = False
+    back = keep.clone()
+    keep[:, cols] = False
+    back[:, wcols] = False
+    assert torch.equal(h[keep], h0[keep])
+    for half in (slice(0, F), slice(F, 2 * F)):
+        assert torch.equal(d[:, half][back], d0[:, half][back])
+    if fmt == MX:   # the NVFP4 products take the scale code without a value, which no cast writes, as 480
+        assert torch.isnan(h[rows]).all() and torch.isnan(d[rows]).all()
