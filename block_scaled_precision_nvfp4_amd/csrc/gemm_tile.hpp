@@ -1077,7 +1077,6 @@ __device__ __forceinline__ void nvw_main_loop(const G& g, int64_t m0, int64_t n0
 // reaches the sums.
 constexpr int NVS_STAGE = NV4_CODES + 2 * GBM * NVS_REC;   // 38 KiB
 static_assert(4 * NVS_STAGE <= Fmt<3>::LDS, "NVFP4 per-slice scale LDS");
-static_assert(NVS_DS * 64 * 4 == 2 * GBM * 3, "the records of a slice: 4 waves x 6 DMAs of 64 dwords");
 
 // Code DMAs of part P of the slice whose first code byte per row is b0; in the slice that K
 // ends inside (tail, uniform) every lane checks its chunk and carries the whole offset in the
