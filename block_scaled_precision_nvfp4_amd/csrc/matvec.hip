@@ -184,8 +184,10 @@ __device__ __forceinline__ void mv_scales(const MvArgs& a, float (&s0)[NW]) {
 // ---------------------------------------------------------------- one token
 
 // One chunk of x: A's row i holds the chunk's block i and zeros elsewhere, so the product's row i is block
-// i's sum, over unscaled weights, and accumulator r of lane group g is block 4g + r, whose scale is byte
-// r of the lane's own.  That leaves half a VALU operation per weight and four per chunk for the scales.
+// i's sum, over weights without their scale, and accumulator r of lane group g is block 4g + r, whose scale
+// is byte r of the lane's own.  That leaves half a VALU operation per weight and six per chunk for the scales.
+// The weights of a block's sum are code * 2^-7 (exact in bf16), at most 6/128 each, so that 16 of them times
+// finite tokens stay below the largest token; its scale takes the 2^7 back (at most 448 * 128).
 // Lane (i, g) holds x where i / 4 = g, in the steps 2 (i % 4) and 2 (i % 4) + 1.
 struct MvOneX {
     bf16x8_t v[2];
@@ -198,11 +200,13 @@ struct MvOneX {
     }
 };
 
+constexpr float MV_CODE_SCALE = 128.0f;
+
 __device__ __forceinline__ bf16x8_t mv_codes(uint32_t w) {
     bf16x8_t r;
     static_for<0, 4>([&](auto i_c) {
         constexpr int I = decltype(i_c)::value;
-        const bf16x2_t v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, I);
+        const bf16x2_t v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f / MV_CODE_SCALE, I);
         r[2 * I] = v[0];
         r[2 * I + 1] = v[1];
     });
@@ -222,11 +226,14 @@ __device__ __forceinline__ void mv_use_one(const MvPiece (&p)[NW], const MvOneX&
             d[o] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, mv_codes(mv_word<J>(p[o])), J == 0 ? zero : d[o], 0, 0, 0);
     });
 #pragma unroll
-    for (int o = 0; o < NW; ++o)
-        static_for<0, 4>([&](auto r_c) {
-            constexpr int R = decltype(r_c)::value;
-            acc[o][R] = __builtin_fmaf(d[o][R], __builtin_amdgcn_cvt_f32_fp8((int)p[o].scales, R), acc[o][R]);
-        });
+    for (int o = 0; o < NW; ++o) {
+        const floatx2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(p[o].scales, MV_CODE_SCALE, false);
+        const floatx2 hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(p[o].scales, MV_CODE_SCALE, true);
+        acc[o][0] = __builtin_fmaf(d[o][0], lo[0], acc[o][0]);
+        acc[o][1] = __builtin_fmaf(d[o][1], lo[1], acc[o][1]);
+        acc[o][2] = __builtin_fmaf(d[o][2], hi[0], acc[o][2]);
+        acc[o][3] = __builtin_fmaf(d[o][3], hi[1], acc[o][3]);
+    }
 }
 
 constexpr int MV_ONE_WAVES = 16;

@@ -201,3 +201,25 @@ def test_weights_past_2_to_the_32_bytes(M):
     rows = torch.tensor([0, 15, 16, 261870, 261888, 523760, 523776, N - 17, N - 1], device=DEV)
     want, S = product(x.cpu().double(), nvfp4_values(codes[rows], scales[rows], s[rows]))
     assert_within(y[:, rows], want, sum_error(K, S) + store_error(want, torch.float32), "y")
+
+
+# values whose products with the codes alone leave fp32's range, while the weights (codes times scales) keep them in it
+@pytest.mark.parametrize("M", [1, 3])
+@pytest.mark.parametrize("N,K", [(40, 48), (33, 256), (70, 528)])
+def test_largest_tokens_times_small_scales(M, N, K):
+    g = torch.Generator().manual_seed(90)
+    x = (torch.randn((M, K), generator=g).clamp(-3, 3) * 2.0 ** 126).to(torch.bfloat16).to(DEV)   # |x| < 2^128
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8).to(DEV)
+    scales = torch.randint(1, 3, (N, K // 16), generator=g, dtype=torch.uint8).to(DEV)   # 2^-9 and 2^-8
+    w = (codes, scales, torch.full((1,), 2.0 ** 10, device=DEV))
+    want, S = product(x.cpu().double(), nvfp4_values(*w))
+    assert float(S.max()) * 2.0 ** 10 < 2.0 ** 128   # no partial sum of the products leaves the range
+    for dt in (torch.float32, torch.bfloat16):
+        y = bsq.nvfp4_matvec(x, *w, out_dtype=dt)
+        assert_within(y, want, sum_error(K, S) + store_error(want, dt), "y")
+    s = torch.full((1,), 2.0 ** 115, device=DEV)
+    gate, up = product(x.cpu().double(), nvfp4_values(codes, scales, s)), product(x.cpu().double(), nvfp4_values(codes, scales, s))
+    h = bsq.nvfp4_gated_matvec(bsq.ACT_SILU, x, codes, scales, s, codes, scales, s)
+    want = act64(gate[0], 0)[0] * up[0]
+    e = gated_error(gate[0], up[0], sum_error(K, gate[1]), sum_error(K, up[1]), 0)
+    assert_within(h, want, e * (1 + 2.0 ** -8) + store_error(want, torch.bfloat16), "h")
