@@ -159,20 +159,14 @@ __global__ __launch_bounds__(GRAD_THREADS) void grad_finish_kernel(const double*
 }
 
 // c = min(1, max_norm / (N + 1e-6)); NaN stays NaN (a NaN among the gradients, or infinite ones times 0).
-__device__ __forceinline__ float clip_factor(double sumsq, double max_norm) {
+__device__ __forceinline__ double clip_factor(double sumsq, double max_norm) {
     const double c = max_norm / (sqrt(sumsq) + 1e-6);
-    return c > 1.0 ? 1.0f : (float)c;
+    return c > 1.0 ? 1.0 : c;
 }
 
-// sums: `n` slots to add (1: the sum itself).
-template <class T>
-__global__ __launch_bounds__(GRAD_THREADS) void grad_clip_kernel(T t, const double* sums, int n, double max_norm,
-                                                                 float* norm) {
-    __shared__ double red[GRAD_THREADS / 64];
-    const double s = n == 1 ? *sums : sum_parts(sums, n, red);
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)sqrt(s);
-    const float c = clip_factor(s, max_norm);
-    if (std::is_same<T, GradList>::value && c == 1.0f) return;   // in place: every gradient keeps its bits
+// Every gradient of this workgroup's chunks replaced by, or written out as, scale(gradient).
+template <class T, class F>
+__device__ __forceinline__ void scale_chunks(const T& t, F&& scale) {
     for_chunks<true>(t, [&](int i, int64_t e0, int n) {
         if (t.last[i] & GRAD_BF16) {
             const uint16_t* p = (const uint16_t*)t.src[i] + e0;
@@ -181,10 +175,10 @@ __global__ __launch_bounds__(GRAD_THREADS) void grad_clip_kernel(T t, const doub
                 n, [&](int v) { return *(const GradB8*)(p + 8 * v); },
                 [&](int v, GradB8 x) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) x.w[k] = bf16x2_rne(bf16_lo(x.w[k]) * c, bf16_hi(x.w[k]) * c);
+                    for (int k = 0; k < 4; ++k) x.w[k] = bf16x2_rne(scale(bf16_lo(x.w[k])), scale(bf16_hi(x.w[k])));
                     *(GradB8*)(q + 8 * v) = x;
                 },
-                [&](int e) { q[e] = (uint16_t)bf16x2_rne(bf16_value(p[e]) * c, 0.0f); });
+                [&](int e) { q[e] = (uint16_t)bf16x2_rne(scale(bf16_value(p[e])), 0.0f); });
         } else {
             const float* p = (const float*)t.src[i] + e0;
             float* q = (float*)t.out(i) + e0;
@@ -192,12 +186,30 @@ __global__ __launch_bounds__(GRAD_THREADS) void grad_clip_kernel(T t, const doub
                 n, [&](int v) { return *(const GradF4*)(p + 4 * v); },
                 [&](int v, GradF4 x) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) x.v[k] *= c;
+                    for (int k = 0; k < 4; ++k) x.v[k] = scale(x.v[k]);
                     *(GradF4*)(q + 4 * v) = x;
                 },
-                [&](int e) { q[e] = p[e] * c; });
+                [&](int e) { q[e] = scale(p[e]); });
         }
     });
+}
+
+// sums: `n` slots to add (1: the sum itself).  c is rounded to binary32, except below its normal range (norms
+// above 2^126 max_norm), where it would lose bits, or be 0, while its products are still normal values.
+template <class T>
+__global__ __launch_bounds__(GRAD_THREADS) void grad_clip_kernel(T t, const double* sums, int n, double max_norm,
+                                                                 float* norm) {
+    __shared__ double red[GRAD_THREADS / 64];
+    const double s = n == 1 ? *sums : sum_parts(sums, n, red);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)sqrt(s);
+    const double cd = clip_factor(s, max_norm);
+    if (cd > 0.0 && cd < 0x1p-126) {
+        scale_chunks(t, [&](float v) { return (float)((double)v * cd); });
+        return;
+    }
+    const float c = (float)cd;
+    if (std::is_same<T, GradList>::value && c == 1.0f) return;   // in place: every gradient keeps its bits
+    scale_chunks(t, [&](float v) { return v * c; });
 }
 
 // Fills the table with tensors from `at` on; returns the first one that it leaves out.

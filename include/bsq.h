@@ -491,7 +491,9 @@ int blockscaled_gated_gemm_backward(int fmt, int act, int64_t M, int64_t F, int6
 /*
  * grad_sumsq / grad_clip / clip_grad_norm -- the global 2-norm of a list of gradients, and the gradients scaled so
  * that it does not exceed max_norm: N = sqrt(sum of all squares), c = min(1, max_norm / (N +
- * 1e-6)), out = c * grad rounded once (RNE) to the gradient's type.  Two calls, so that ranks that
+ * 1e-6)), out = c * grad.  c is computed in binary64 and rounded to binary32 (not below 2^-126, where that
+ * would cost it bits), the product to binary32, and for bf16 gradients then to bf16 (all RNE).
+ * Two calls, so that ranks that
  * hold different gradients can add up their sums in between; clip_grad_norm is both in one, with
  * the same results and one launch less.
  *   grads, outs, numels, dtypes  HOST arrays of count entries, read before the call returns:

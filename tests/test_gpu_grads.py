@@ -201,3 +201,21 @@ def test_a_tensor_past_2_to_the_31_elements():
     c = 1.0 / (want + 1e-6)
     for i, v in ((0, 0.5), (1 << 30, 0.5), ((1 << 31) - 1, 0.5), (1 << 31, 0.5), (n - 2, 0.5), (n - 1, 2.0)):
         assert abs(float(g[i]) - v * c) <= v * c * (2.0 ** -8 + 2.0 ** -20), i
+
+
+# a factor below fp32's normal range: the gradients it scales are large enough for their products to matter
+@pytest.mark.parametrize("max_norm", [1e-3, 1e-6, 1e-9])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_factor_below_the_normal_range(max_norm, in_place):
+    g = torch.Generator().manual_seed(24)
+    v = torch.randn(9001, generator=g).clamp(-3, 3)
+    grads = [(v * 1e38).to(DEV), (v[:777] * 9e37).to(torch.bfloat16).to(DEV), torch.ones(5, device=DEV)]
+    before = [t.cpu().double() for t in grads]
+    n = math.sqrt(math.fsum(float(t.square().sum()) for t in before))
+    out = grads if in_place else [torch.empty_like(t) for t in grads]
+    bsq.clip_grad_norm(grads, max_norm, out=None if in_place else out)
+    for i, (b, o) in enumerate(zip(before, out)):
+        want = b * (max_norm / (n + 1e-6))
+        rel = 2.0 ** -8 * (1 + 2.0 ** -14) if o.dtype == torch.bfloat16 else 2 * 2.0 ** -24
+        tiny = 2.0 ** -134 if o.dtype == torch.bfloat16 else 2.0 ** -149
+        assert_within(o, want, want.abs() * rel + tiny, "gradient %d" % i)
