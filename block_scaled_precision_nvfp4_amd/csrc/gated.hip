@@ -383,13 +383,30 @@ static int with_loop(int fmt, int64_t K, int slab, F&& launch) {
 }
 
 // Whether 64 x 64 tiles (gated_small.hip) are faster than `tiles` of these.  They fill the chip where these
-// leave it idle, but read their operands 4 times as often and, in MXFP8, feed the MFMA far less well than the
-// large tile's aligned loops.  us large / small, forward NVFP4: 63 / 12 at 16 tiles (333 x 1003 x 2080), 79 / 38
-// at 32 (1024 x 1024 x 4096), 30 / 25 at 64, 34 / 45 at 128; MXFP8: 24 / 7 at 16, 47 / 53 at 32, 28 / 26 at 68
-// with K = 1056 (the loop without aligned records is the slower one).  Backward NVFP4: 88 / 13 at 8, 42 / 33 at 64, 48 / 58
-// at 128; MXFP8: 48 / 29 at 16, 25 / 17 at 32, 27 / 32 at 64.
-static bool use_small(int fmt, int64_t K, int64_t tiles, bool backward) {
-    return tiles <= (fmt == 0 || K % (MX_GROUP * 64) != 0 ? 64 : backward ? 32 : 24);
+// leave it idle, but read their operands 4 times as often.  16 large tiles are 256 small ones, one per CU; two
+// share a CU, and a small launch takes the longer the more such rounds of 16 there are, while a large one takes
+// the same until its tiles outnumber the CUs.  NVFP4, whose large loops with K % 256 != 0 are the slower ones:
+// a number of rounds.  MXFP8: a round costs time in proportion to K, a large tile a constant too, so the
+// rounds that pay fall as a + b / K, with a and b fitted to each loop, up to 6.
+// us large / small, silu, gate and up kept, operands in the caches:
+//   NVFP4 K = 1024   forward 30 / 24 at 64 tiles, 30 / 28 at 68, 31 / 34 at 96; backward 42 / 39 at 80, 43 / 45 at 96
+//   NVFP4 K = 4096   forward 80 / 71 at 64, 80 / 83 at 68; backward 93 / 91 at 80, 94 / 107 at 96
+//   NVFP4 K = 1056   forward 40 / 31 at 96, 41 / 41 at 128; backward 48 / 43 at 96, 51 / 55 at 128
+//   NVFP4 K = 4064   forward 94 / 93 at 96, 95 / 120 at 128; backward 103 / 102 at 96, 105 / 132 at 128
+//   MXFP8 K = 512    forward 17 / 17 at 64, 17 / 20 at 68; backward 22 / 20 at 64, 23 / 24 at 68
+//   MXFP8 K = 1024   forward 20 / 16 at 32, 20 / 22 at 40; backward 25 / 17 at 32, 26 / 24 at 48
+//   MXFP8 K = 4096   forward 42 / 28 at 16, 46 / 51 at 24; backward 48 / 29 at 16, 52 / 52 at 24
+//   slab K = 1024    forward 21 / 18 at 48, 21 / 22 at 64; backward 27 / 20 at 48, 27 / 27 at 64
+//   slab K = 4096    forward 46 / 38 at 32, 46 / 52 at 40; backward 50 / 39 at 32, 52 / 53 at 40
+//   MXFP8 K = 544    forward 22 / 20 at 96, 23 / 28 at 128; backward 29 / 27 at 96, 30 / 37 at 128
+//   MXFP8 K = 1056   forward 28 / 27 at 80, 29 / 32 at 96; backward 33 / 32 at 80, 35 / 37 at 96
+//   MXFP8 K = 4064   forward 71 / 69 at 48, 71 / 91 at 64; backward 77 / 72 at 48, 77 / 94 at 64
+static bool use_small(int fmt, int64_t K, int slab, int64_t tiles, bool backward) {
+    const int64_t rounds = (tiles + 15) / 16;
+    if (fmt == 0) return rounds <= (K % 256 != 0 ? 6 : backward ? 5 : 4);
+    if (rounds > 6) return false;
+    if (K % (MX_GROUP * 64) != 0) return (10 * rounds - 28) * K <= 24000;   // rounds <= 2.8 + 2400 / K
+    return slab ? (10 * rounds - 27) * K <= 9000 : (10 * rounds - 16) * K <= 12500;
 }
 
 int64_t gated_tiles(int64_t M, int64_t N) { return ((M + GBM - 1) / GBM) * ((N + GBN / 2 - 1) / (GBN / 2)); }
@@ -421,7 +438,7 @@ int launch_gated_gemm(int fmt, int act, int64_t M, int64_t N, int64_t K, const u
     g.u_s_enc = up_s_enc;
     g.gate_up = (uint16_t*)gate_up;
     g.act = act;
-    if (use_small(fmt, K, gated_tiles(M, N), false)) return launch_gated_small(fmt, g, hip_stream);
+    if (use_small(fmt, K, slab, gated_tiles(M, N), false)) return launch_gated_small(fmt, g, hip_stream);
     const int64_t p = fmt == 0 ? persistent_workgroups(g) : 0;
     if (p > 0) {
         const auto launch = [&](auto save, auto a) {
@@ -450,7 +467,7 @@ int launch_gated_gemm_backward(int fmt, int act, int64_t M, int64_t N, int64_t K
     g.gate_up = (const uint16_t*)gate_up;
     g.act = act;
     const int64_t tiles = ((M + GBM - 1) / GBM) * ((N + GBN - 1) / GBN);
-    if (use_small(fmt, K, tiles, true)) return launch_gated_backward_small(fmt, g, hip_stream);
+    if (use_small(fmt, K, slab, tiles, true)) return launch_gated_backward_small(fmt, g, hip_stream);
     return with_loop(fmt, K, slab, [&](auto f, auto mode, auto sl) {
         hipLaunchKernelGGL((gated_backward_kernel<decltype(f)::value, decltype(mode)::value, decltype(sl)::value>),
                            dim3((unsigned)tiles), dim3(256), 0, (hipStream_t)hip_stream, g);

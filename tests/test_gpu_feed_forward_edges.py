@@ -1,5 +1,6 @@
 """Edges of the feed-forward operators: stores of the large tiles and of the token kernels stay inside their
-outputs, and values that are not finite go where the binary64 form has them.
+outputs, values that are not finite go where the binary64 form has them, and the gated products around the sizes
+where one tile hands over to the other.
 
 The guarded outputs lie in a buffer with at least a tile's rows before and after them, filled with a value
 that no output takes; the results are those of the same call on buffers of its own, bit for bit."""
@@ -9,7 +10,7 @@ import torch
 import block_scaled_precision_nvfp4_amd as bsq
 from tests.gpu_common import note
 from tests.plain64 import assert_within, nvfp4_values, product, store_error, sum_error
-from tests.test_gpu_gated import AR, BR, DEV, MX, NV, SLAB, operand
+from tests.test_gpu_gated import AR, BR, DEV, MX, NV, SLAB, backward, forward, gauss, operand
 from tests.test_gpu_matvec import tokens, weights
 
 pytestmark = pytest.mark.gpu
@@ -119,3 +120,45 @@ def test_gated_tokens_that_are_not_finite(M, K):
         bad[2] = True
         h = bsq.nvfp4_gated_matvec(bsq.ACT_SILU, x, *wg, *wu).cpu()
         assert torch.equal(torch.isnan(h), bad) and torch.equal(h[~bad], clean[~bad])
+
+
+# the last size that the 64 x 64 tiles take and the next one, of each loop, and large ones of the loops whose
+# change-over lies highest
+@pytest.mark.parametrize("fmt,M,F,K", [(NV, 1024, 2048, 256), (NV, 1024, 2049, 256), (NV, 2048, 1536, 288), (NV, 2049, 1536, 288),
+                                       (MX, 2048, 1024, 512), (MX, 2049, 1024, 512), (MX, 1024, 512, 4096), (MX, 1024, 513, 4096),
+                                       (MX, 2048, 1280, 1056), (MX, 2049, 1280, 1056), (MX, 2048, 1536, 544), (MX, 2049, 1536, 544),
+                                       (MX | SLAB, 1536, 1024, 1024), (MX | SLAB, 1537, 1024, 1024),
+                                       (MX | bsq.FMT_MX_SLAB_B, 1024, 1024, 4096), (MX | bsq.FMT_MX_SLAB_B, 1025, 1024, 4096)])
+def test_forward_around_the_change_of_tiles(fmt, M, F, K):
+    forward(fmt, K % 3, M, F, K, True, most=96)
+
+
+@pytest.mark.parametrize("fmt,M,F,K", [(NV, 2048, 2560, 256), (NV, 2049, 2560, 256), (NV, 1536, 4096, 288), (NV, 1537, 4096, 288),
+                                       (MX, 2048, 2048, 512), (MX, 2049, 2048, 512), (MX, 1024, 1024, 4096), (MX, 1025, 1024, 4096),
+                                       (MX, 2048, 2560, 1056), (MX, 2049, 2560, 1056), (MX, 1536, 4096, 544), (MX, 1537, 4096, 544),
+                                       (MX | SLAB, 1536, 2048, 1024), (MX | SLAB, 1537, 2048, 1024),
+                                       (MX | bsq.FMT_MX_SLAB_A, 1024, 2048, 4096), (MX | bsq.FMT_MX_SLAB_A, 1025, 2048, 4096),
+                                       (NV, 2305, 2571, 288), (NV | AR, 2305, 2568, 96), (MX, 2305, 2563, 544),
+                                       (MX, 2305, 2568, 160)])
+def test_backward_around_the_change_of_tiles(fmt, M, F, K):
+    backward(fmt, K % 3, M, F, K, most=96)
+
+
+# K-blocks even and odd, slices even and odd, K ending inside a slice; the size takes the large tiles
+@pytest.mark.parametrize("fmt,K", [(NV, 512), (NV, 544), (NV, 96), (MX, 512), (MX, 544), (MX, 576), (MX, 608), (MX, 160)])
+def test_scales_that_are_not_finite_in_the_backward_of_large_tiles(fmt, K):
+    M, F = 2566, 2057
+    dy, w, gu = operand(fmt, 0, 0, M, K, 0.5, 4), operand(fmt, 0, 0, F, K, 0.5, 5), gauss(M, 2 * F, 1.0, 6)
+    d0 = bsq.blockscaled_gated_gemm_backward(fmt, 0, *dy, *w, gu).cpu()
+    nan, last = 0x7F if fmt == NV else 0xFF, dy[1].shape[1] - 1
+    dy[1][3, 0] = dy[1][259, 1] = dy[1][2561, last] = nan
+    w[1][5, 0] = w[1][200, last] = w[1][1030, 1] = nan
+    d = bsq.blockscaled_gated_gemm_backward(fmt, 0, *dy, *w, gu).cpu()
+    rows, cols = [3, 259, 2561], [5, 200, 1030]
+    keep = torch.ones((M, F), dtype=torch.bool)
+    keep[rows] = False
+    keep[:, cols] = False
+    for half in (slice(0, F), slice(F, 2 * F)):
+        assert torch.equal(d[:, half][keep], d0[:, half][keep])
+    if fmt == MX:   # the NVFP4 products take the scale code without a value as 480
+        assert torch.isnan(d[rows]).all() and torch.isnan(d[:, cols]).all()
