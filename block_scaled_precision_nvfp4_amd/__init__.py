@@ -3,7 +3,8 @@
 Thin ctypes marshalling over the C ABI in include/bsq.h: every step of the computation
 runs in the library's HIP kernels.  PyTorch only provides device memory (output
 tensors are allocated with torch.empty) and the current HIP stream.  The functions
-have the names of the C entry points.  Importing works without a GPU; calling a
+have the names of the C entry points and are not recorded by autograd: results have no
+history.  Importing works without a GPU; calling a
 compute function needs libbsq.so (built by ``python -m
 block_scaled_precision_nvfp4_amd.build``) and fails loudly if it is missing.
 """
@@ -645,7 +646,7 @@ class _GradList:
 
 
 def grad_sumsq(grads: Sequence[torch.Tensor], workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """The sum of squares over all gradients (bf16 and float32 tensors) as a float64[1] device tensor; ranks
+    """The sum of squares over all gradients (contiguous bf16 and float32 tensors) as a float64[1] device tensor; ranks
     that hold different gradients add theirs up before ``grad_clip``."""
     g = _GradList(grads)
     ws = g.workspace(workspace)
@@ -670,7 +671,7 @@ def grad_clip(grads: Sequence[torch.Tensor], sumsq: torch.Tensor, max_norm: floa
 def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional[Sequence[torch.Tensor]] = None,
                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gradients' global 2-norm (float32[1], on the device), and the gradients scaled so that it does not
-    exceed ``max_norm``, in place or into ``out``.  ``workspace``: at least grad_workspace_bytes(len(grads))
+    exceed ``max_norm``, in place or into ``out``.  The tensors are contiguous bf16 or float32.  ``workspace``: at least grad_workspace_bytes(len(grads))
     bytes of scratch; one is allocated when none is given."""
     g = _GradList(grads, out)
     ws = g.workspace(workspace)

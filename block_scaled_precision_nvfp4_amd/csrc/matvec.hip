@@ -12,11 +12,17 @@
 // binary32.  The only roundings are those sums, a block's scale where it is applied to a block's sum, one
 // division by the tensor (or row) scale and the output's.
 //
-// Measured in a graph, weights rotating through 600 MB: one token, 4096 x 14336 9.9 us (3.3 TB/s of weights, a
-// large copy on this card moves 4.7), 16384 x 16384 34.4 us (4.4 TB/s), gated 14336 x 4096 16.5 us (4.0
-// TB/s); 16 tokens, 4096 x 14336 18.1 us, gated 14336 x 4096 24.8 us; 64 tokens, gated 14336 x 8192 63 us. The
-// smallest, 1 x 256 x 256, takes 2.2 us. What is left at these sizes is the way in and out: the launch, the
-// first trip to memory, the join.
+// us in a graph, weights rotating through 800 MB (the same weights again and again, in part from the caches, in
+// brackets); a large copy on this card moves 4.7 TB/s:
+//   1 token    4096 x 4096 5.1 (4.3), 4096 x 14336 9.5 (8.4), 16384 x 16384 33.7 (30.3): 3.5 and 4.5 TB/s of
+//              weights in the last two; gated 14336 x 4096 16.0 (15.2), 4.1 TB/s
+//   4 tokens   4096 x 4096 6.8 (6.0), 4096 x 14336 14.1 (12.3)
+//   8          4096 x 4096 7.7 (6.5), 4096 x 14336 15.4 (13.9), gated 14336 x 4096 22.4 (19.3)
+//   16         4096 x 4096 8.6 (7.6), 4096 x 14336 17.5 (16.3), gated 14336 x 4096 23.9 (21.1)
+//   64         4096 x 4096 13.0 (11.7), gated 14336 x 8192 62 (56)
+// The smallest, 1 x 256 x 256, takes 2.2.  What is left for one token is the way in and out: the launch, the
+// first trip to memory, the join.  Several are held back by one workgroup of 8 waves per CU (its tokens take
+// 132 KiB of LDS from 16 on) that meets at a barrier after every chunk.
 #include "activation.hpp"
 #include "launch.hpp"
 
@@ -469,10 +475,11 @@ static int launch_tokens(MvArgs a, hipStream_t s) {
     return (int)hipGetLastError();
 }
 
-// Tiles of as many tokens as leave three CUs in four a workgroup: a larger one dequantizes a weight fewer
-// times (64 x 14336 x 8192 gated: 63 us with 64, 186 with tokens read by every wave), a smaller one splits
-// into more workgroups (64 x 4096 x 4096: 12.9 us with 32, 23.8 with 64; 33 x 1000 x 16384: 17.5 with
-// 16, 62 with 64).
+// Tiles of as many tokens as leave three CUs in four a workgroup: a larger one reads and dequantizes a weight
+// fewer times, a smaller one splits into more workgroups.  us with tiles of 16 / 32 / 64, weights rotating:
+// 64 x 14336 x 8192 gated 142 / 88 / 61, 64 x 14336 x 4096 54 / 34 / 25; 64 x 6151 x 4112 31 / 21 / 28, 64 x
+// 4096 x 4096 15 / 13 / 24, 32 x 14336 x 4096 28 / 19 / 21; 32 x 4096 x 4096 11 / 13 / 20, 33 x 1000 x
+// 16384 17 / 31 / 63.
 template <bool GATED, int LOAD>
 static int launch_mv(const MvArgs& a, hipStream_t s) {
     if (a.M == 1) return launch_one<GATED, LOAD>(a, s);
