@@ -7,7 +7,7 @@
 // chunk), whole 128-byte lines of each row, and loads the next chunks before it uses the current one.  K
 // is split over the waves of a workgroup and joined in LDS.
 //
-// x is bf16 as it comes, and so is every weight: E2M1 alone, or E2M1 * E4M3, which has at most 6
+// x is bf16 as it comes, and so is every weight: E2M1 * 2^-7, or E2M1 * E4M3, which has at most 6
 // significant bits and lies in [2^-10, 2688].  The bf16 MFMA multiplies exactly and accumulates in
 // binary32.  The only roundings are those sums, a block's scale where it is applied to a block's sum, one
 // division by the tensor (or row) scale and the output's.
