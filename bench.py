@@ -66,6 +66,7 @@ GEMM_SOURCES = ("block_scaled_precision_nvfp4_amd/csrc/gemm.hip",
                 "block_scaled_precision_nvfp4_amd/csrc/gemm_tile.hpp",
                 "block_scaled_precision_nvfp4_amd/csrc/device_common.hpp")
 QUANT_SOURCES = ("block_scaled_precision_nvfp4_amd/csrc/quantize.hip",
+                 "block_scaled_precision_nvfp4_amd/csrc/encode.hpp",
                  "block_scaled_precision_nvfp4_amd/csrc/device_common.hpp")
 # HBM traffic per launch (hardware counters) of the kernels the line reports a roofline for:
 # the summary under profiles/ and the sources it was taken on

@@ -81,7 +81,22 @@ def lib():
         L.grad_sumsq.argtypes = [vp, vp, vp, i64, vp, vp, vp]
         L.grad_clip.argtypes = [vp, vp, vp, vp, i64, vp, C.c_double, vp, vp]
         L.clip_grad_norm.argtypes = [vp, vp, vp, vp, i64, C.c_double, vp, vp, vp]
-        for f in ("nvfp4_matvec", "nvfp4_gated_matvec", "blockscaled_gated_gemm", "blockscaled_gated_gemm_backward",
+        L.moe_sort_rows.argtypes = [i64, i64, i64]
+        L.moe_sort_rows.restype = C.c_int64
+        L.moe_sort_workspace_bytes.argtypes = [i64, i64]
+        L.moe_sort_workspace_bytes.restype = C.c_int64
+        L.moe_sort.argtypes = [vp, i32, i64, i64, i64, i64, vp, vp, vp, vp, vp]
+        L.moe_gather.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, vp, vp]
+        L.moe_gather_nvfp4_rowscaled.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, vp, vp]
+        L.moe_gather_mxfp8.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, vp]
+        L.moe_combine.argtypes = [i64, i64, i64, vp, i32, i64, vp, vp, vp, i32, vp]
+        L.moe_combine_backward.argtypes = [i64, i64, i64, vp, vp, i32, i64, vp, vp, vp, vp, vp, vp]
+        L.lora_workspace_bytes.argtypes = [i64, i64]
+        L.lora_workspace_bytes.restype = C.c_int64
+        L.lora_add.argtypes = [i64, i64, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, i32, vp, vp]
+        L.nvfp4_lora_matvec.argtypes = [i32, i64, i64, i64, vp, i64, vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, i32, vp, vp]
+        for f in ("moe_sort", "moe_gather", "moe_gather_nvfp4_rowscaled", "moe_gather_mxfp8", "moe_combine",
+                  "moe_combine_backward", "lora_add", "nvfp4_lora_matvec", "nvfp4_matvec", "nvfp4_gated_matvec", "blockscaled_gated_gemm", "blockscaled_gated_gemm_backward",
                   "grad_sumsq", "grad_clip", "clip_grad_norm", "nvfp4_linear_forward", "nvfp4_linear_backward", "nvfp4_quantize",
                   "nvfp4_quantize_noalloc",
                   "nvfp4_col_mxfp8_row_quantize", "nvfp4_quantize_fprop_wgrad", "nvfp4_quantize_rowscaled",
@@ -679,3 +694,246 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
     _check("clip_grad_norm", lib().clip_grad_norm(*g.args(), max_norm, norm.data_ptr(), ws.data_ptr(),
                                                   _stream(g.device)))
     return norm
+
+
+# ---------------------------------------------------------------- tokens and their experts
+
+_TYPES = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
+
+
+def _type(dtype: torch.dtype, name: str) -> int:
+    if dtype not in _TYPES:
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, dtype))
+    return _TYPES[dtype]
+
+
+def _on(t: torch.Tensor, dev, name: str):
+    if t.device != dev:
+        raise ValueError("%s must be on %s" % (name, dev))
+
+
+def _rows(x: torch.Tensor, dtype, name: str):
+    """x [rows, columns] of a type with adjacent elements in a row; returns (rows, columns, elements between rows)."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError("%s must be a CUDA/HIP tensor" % name)
+    if dtype is not None and x.dtype != dtype:
+        raise TypeError("%s must have dtype %s, got %s" % (name, dtype, x.dtype))
+    if x.dim() != 2:
+        raise ValueError("%s must have two dimensions" % name)
+    R, C_ = x.shape
+    if C_ > 1 and x.stride(1) != 1:
+        raise ValueError("%s must have adjacent elements in a row" % name)
+    return R, C_, x.stride(0) if R > 1 else -(-C_ // 8) * 8
+
+
+def _slots(positions: torch.Tensor, T: int, dev) -> int:
+    """positions [T, k]; returns k."""
+    _dev_tensor(positions, torch.int32, "positions")
+    _on(positions, dev, "positions")
+    if positions.dim() != 2 or positions.shape[0] != T:
+        raise ValueError("positions must be [%d, k], got %s" % (T, tuple(positions.shape)))
+    return positions.shape[1]
+
+
+def _source(source: torch.Tensor, dev) -> int:
+    _dev_tensor(source, torch.int32, "source")
+    _on(source, dev, "source")
+    if source.dim() != 1:
+        raise ValueError("source must have one dimension")
+    return source.shape[0]
+
+
+def moe_sort(experts: torch.Tensor, num_experts: int, align: int = 1,
+             workspace: Optional[torch.Tensor] = None) -> Dict[str, torch.Tensor]:
+    """The order of token slots by expert for ``blockscaled_grouped_gemm``.  ``experts`` [T, k] (int32 or int64) holds each
+    slot's expert; slots with ids outside [0, num_experts) are dropped.  Returns ``offsets`` (int64
+    [num_experts + 1], each group starting at a multiple of ``align``; GROUP_K needs 32), ``positions`` (int32 [T, k], a
+    slot's row or -1) and ``source`` (int32 [rows], a row's slot t k + j or -1), where rows holds any choice of
+    experts.  ``workspace``: lib().moe_sort_workspace_bytes(T k, num_experts) bytes of scratch; one is allocated when
+    none is given."""
+    if not isinstance(experts, torch.Tensor) or experts.dtype not in (torch.int32, torch.int64):
+        raise TypeError("experts must be an int32 or int64 tensor")
+    _dev_tensor(experts, experts.dtype, "experts")
+    if experts.dim() != 2:
+        raise ValueError("experts must be [tokens, k]")
+    dev, n, L = experts.device, experts.numel(), lib()
+    rows, need = L.moe_sort_rows(n, num_experts, align), L.moe_sort_workspace_bytes(n, num_experts)
+    ws = _workspace(workspace, max(need, 0), dev)
+    offsets = torch.empty(max(num_experts, 0) + 1, dtype=torch.int64, device=dev)
+    positions = torch.empty(experts.shape, dtype=torch.int32, device=dev)
+    source = torch.empty(max(rows, 0), dtype=torch.int32, device=dev)
+    _check("moe_sort", L.moe_sort(experts.data_ptr(), experts.element_size(), n, num_experts, align, rows,
+                                  offsets.data_ptr(), positions.data_ptr(), source.data_ptr(), ws.data_ptr(), _stream(dev)))
+    return {"offsets": offsets, "positions": positions, "source": source}
+
+
+def moe_gather(x: torch.Tensor, positions: torch.Tensor, source: torch.Tensor,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Tokens x [T, H] (bf16; rows may be strided) in the order of ``moe_sort``: [rows, H] bf16, zeros in rows without a
+    token.  Its gradient is ``moe_combine(d, positions)``."""
+    T, H, ldx = _rows(x, torch.bfloat16, "x")
+    dev = x.device
+    k, R = _slots(positions, T, dev), _source(source, dev)
+    out = _output(out, (R, H), torch.bfloat16, dev)
+    _check("moe_gather", lib().moe_gather(T, k, H, x.data_ptr(), ldx, positions.data_ptr(), source.data_ptr(), R,
+                                          out.data_ptr(), _stream(dev)))
+    return out
+
+
+def moe_gather_nvfp4_rowscaled(x: torch.Tensor, positions: torch.Tensor, source: torch.Tensor) -> Dict[str, torch.Tensor]:
+    """``nvfp4_quantize_rowscaled(moe_gather(x, positions, source))`` without the copy in between: ``codes`` [rows, H/2],
+    ``scales`` [rows, H/16] (uint8) and ``s_enc`` (float32[rows])."""
+    T, H, ldx = _rows(x, torch.bfloat16, "x")
+    dev = x.device
+    k, R = _slots(positions, T, dev), _source(source, dev)
+    u8 = dict(dtype=torch.uint8, device=dev)
+    out = {"codes": torch.empty((R, H // 2), **u8), "scales": torch.empty((R, H // 16), **u8),
+           "s_enc": torch.empty(R, dtype=torch.float32, device=dev)}
+    _check("moe_gather_nvfp4_rowscaled", lib().moe_gather_nvfp4_rowscaled(
+        T, k, H, x.data_ptr(), ldx, positions.data_ptr(), source.data_ptr(), R, out["codes"].data_ptr(),
+        out["scales"].data_ptr(), out["s_enc"].data_ptr(), _stream(dev)))
+    return out
+
+
+def moe_gather_mxfp8(x: torch.Tensor, positions: torch.Tensor, source: torch.Tensor) -> Dict[str, torch.Tensor]:
+    """``mxfp8_quantize(moe_gather(x, positions, source))`` without the copy in between: ``row_codes`` [rows, H],
+    ``row_scales`` [rows, H/32] (uint8)."""
+    T, H, ldx = _rows(x, torch.bfloat16, "x")
+    dev = x.device
+    k, R = _slots(positions, T, dev), _source(source, dev)
+    u8 = dict(dtype=torch.uint8, device=dev)
+    out = {"row_codes": torch.empty((R, H), **u8), "row_scales": torch.empty((R, H // 32), **u8)}
+    _check("moe_gather_mxfp8", lib().moe_gather_mxfp8(
+        T, k, H, x.data_ptr(), ldx, positions.data_ptr(), source.data_ptr(), R, out["row_codes"].data_ptr(),
+        out["row_scales"].data_ptr(), _stream(dev)))
+    return out
+
+
+def _slot_weights(weights: Optional[torch.Tensor], positions: torch.Tensor):
+    if weights is None:
+        return
+    _dev_tensor(weights, torch.float32, "weights")
+    if weights.shape != positions.shape or weights.device != positions.device:
+        raise ValueError("weights must be %s on %s" % (tuple(positions.shape), positions.device))
+
+
+def moe_combine(y: torch.Tensor, positions: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The experts' rows y [rows, H] (bf16 or float32) back to their tokens: out[t] = sum_j weights[t, j] y[positions[t, j]]
+    (fp32, rounded once) as [T, H] of ``out_dtype`` (bf16 or float32).  ``weights`` [T, k] float32, or None for ones."""
+    if not isinstance(y, torch.Tensor):
+        raise TypeError("y must be a tensor")
+    yt = _type(y.dtype, "y")
+    _dev_tensor(y, y.dtype, "y")
+    if y.dim() != 2:
+        raise ValueError("y must be [rows, H]")
+    dev, (R, H) = y.device, y.shape
+    _dev_tensor(positions, torch.int32, "positions")
+    T = positions.shape[0]
+    k = _slots(positions, T, dev)
+    _slot_weights(weights, positions)
+    ot = _type(out_dtype, "out_dtype")
+    out = _output(out, (T, H), out_dtype, dev)
+    _check("moe_combine", lib().moe_combine(T, k, H, y.data_ptr(), yt, R, positions.data_ptr(), _ptr(weights),
+                                            out.data_ptr(), ot, _stream(dev)))
+    return out
+
+
+def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, positions: torch.Tensor, source: torch.Tensor,
+                         weights: torch.Tensor):
+    """The gradients of ``moe_combine`` for dout [T, H] (bf16): (dy [rows, H] of y's type, zeros in rows without a token;
+    dweights [T, k] float32, 0 for dropped slots)."""
+    _dev_tensor(dout, torch.bfloat16, "dout")
+    if not isinstance(y, torch.Tensor):
+        raise TypeError("y must be a tensor")
+    yt = _type(y.dtype, "y")
+    _dev_tensor(y, y.dtype, "y")
+    if dout.dim() != 2 or y.dim() != 2 or dout.shape[1] != y.shape[1]:
+        raise ValueError("dout must be [T, H] and y [rows, H], got %s and %s" % (tuple(dout.shape), tuple(y.shape)))
+    dev, (T, H) = dout.device, dout.shape
+    _on(y, dev, "y")
+    k, R = _slots(positions, T, dev), _source(source, dev)
+    if y.shape[0] != R:
+        raise ValueError("y has %d rows, source %d" % (y.shape[0], R))
+    _slot_weights(weights, positions)
+    if weights is None:
+        raise TypeError("weights must be a tensor")
+    dy = torch.empty_like(y)
+    dw = torch.empty_like(weights)
+    _check("moe_combine_backward", lib().moe_combine_backward(
+        T, k, H, dout.data_ptr(), y.data_ptr(), yt, R, positions.data_ptr(), source.data_ptr(), weights.data_ptr(),
+        dy.data_ptr(), dw.data_ptr(), _stream(dev)))
+    return dy, dw
+
+
+# ---------------------------------------------------------------- low-rank adapters
+
+def _adapters(adapters: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor, scales: Optional[torch.Tensor], M: int,
+              N: int, K: int, dev):
+    """The adapters' checks; returns (rank, number of adapters)."""
+    _dev_tensor(adapters, torch.int32, "adapters")
+    _dev_tensor(lora_a, torch.bfloat16, "lora_a")
+    _dev_tensor(lora_b, torch.bfloat16, "lora_b")
+    if tuple(adapters.shape) != (M,):
+        raise ValueError("adapters must hold one id per token, got %s" % (tuple(adapters.shape),))
+    if lora_a.dim() != 3 or lora_a.shape[2] != K:
+        raise ValueError("lora_a must be [adapters, rank, %d], got %s" % (K, tuple(lora_a.shape)))
+    n, r = lora_a.shape[0], lora_a.shape[1]
+    if tuple(lora_b.shape) != (n, N, r):
+        raise ValueError("lora_b must be [%d, %d, %d], got %s" % (n, N, r, tuple(lora_b.shape)))
+    if scales is not None:
+        _dev_tensor(scales, torch.float32, "scales")
+        if scales.numel() != n:
+            raise ValueError("scales must hold one value per adapter")
+    for t in (adapters, lora_a, lora_b, scales):
+        if t is not None and t.device != dev:
+            raise ValueError("the adapters and x must be on one device")
+    return r, n
+
+
+def lora_add(y: torch.Tensor, x: torch.Tensor, adapters: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor,
+             scales: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+             workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Each token's low-rank adapter beside a projection's output y [M, N] (bf16 or float32; rows may be strided): y[m] +
+    scales[a] (x[m] A_a^T) B_a^T with a = adapters[m] (int32; ids outside the adapters: none), x [M, K] bf16 (rows may be
+    strided), lora_a [adapters, rank, K] and lora_b [adapters, N, rank] bf16, scales float32 or None for ones.
+    Written to y itself, or to ``out`` [M, N].  ``workspace``: lib().lora_workspace_bytes(M, rank) bytes; one is
+    allocated when none is given."""
+    M, K, ldx = _rows(x, torch.bfloat16, "x")
+    dev = x.device
+    My, N, ldy = _rows(y, None, "y")
+    yt = _type(y.dtype, "y")
+    if My != M or y.device != dev:
+        raise ValueError("y must have x's %d tokens, on its device" % M)
+    r, n = _adapters(adapters, lora_a, lora_b, scales, M, N, K, dev)
+    if out is None:
+        out, ldo = y, ldy
+    else:
+        Mo, No, ldo = _rows(out, y.dtype, "out")
+        if (Mo, No) != (M, N) or out.device != dev:
+            raise ValueError("out must be %s on %s" % ((M, N), dev))
+    ws = _workspace(workspace, max(lib().lora_workspace_bytes(M, r), 0), dev)
+    _check("lora_add", lib().lora_add(M, N, K, r, n, x.data_ptr(), ldx, adapters.data_ptr(), lora_a.data_ptr(),
+                                      lora_b.data_ptr(), _ptr(scales), y.data_ptr(), ldy, out.data_ptr(), ldo, yt,
+                                      ws.data_ptr(), _stream(dev)))
+    return out
+
+
+def nvfp4_lora_matvec(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, w_s_enc: torch.Tensor,
+                      adapters: torch.Tensor, lora_a: torch.Tensor, lora_b: torch.Tensor,
+                      scales: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                      out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``nvfp4_matvec`` with each token's low-rank adapter added before the one rounding of y [M, N]; the adapters as for
+    ``lora_add``."""
+    M, K, ldx = _tokens(x)
+    dev = x.device
+    N, rows = _weights(w_codes, w_scales, w_s_enc, K, "w", dev)
+    r, n = _adapters(adapters, lora_a, lora_b, scales, M, N, K, dev)
+    y_dtype = _type(out_dtype, "out_dtype")
+    out = _output(out, (M, N), out_dtype, dev)
+    ws = _workspace(workspace, max(lib().lora_workspace_bytes(M, r), 0), dev)
+    _check("nvfp4_lora_matvec", lib().nvfp4_lora_matvec(
+        FMT_B_ROWSCALED if rows else 0, M, N, K, x.data_ptr(), ldx, w_codes.data_ptr(), w_scales.data_ptr(),
+        w_s_enc.data_ptr(), r, n, adapters.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(), _ptr(scales), out.data_ptr(),
+        y_dtype, ws.data_ptr(), _stream(dev)))
+    return out

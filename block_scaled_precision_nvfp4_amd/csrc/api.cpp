@@ -670,3 +670,209 @@ int clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* n
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- tokens and their experts
+
+namespace {
+
+bool unaligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+
+int64_t sorted_rows(int64_t n, int64_t E, int64_t align) {
+    return (n + (n < E ? n : E) * (align - 1)) / align * align;
+}
+
+int sort_sizes_check(const char* fn, int64_t slots, int64_t experts, int64_t align) {
+    if (slots < 0 || slots > (int64_t)1 << 30) return fail(BSQ_ERR_SHAPE, "%s: %lld slots are not in [0, 2^30]", fn, (long long)slots);
+    if (experts < 1 || experts > 1024) return fail(BSQ_ERR_SHAPE, "%s: %lld experts are not in [1, 1024]", fn, (long long)experts);
+    if (align < 1 || align > 256 || (align & (align - 1)) != 0)
+        return fail(BSQ_ERR_ARG, "%s: align (%lld) must be a power of two up to 256", fn, (long long)align);
+    return BSQ_OK;
+}
+
+// Sizes shared by the gathers and the combinations.
+int slots_check(const char* fn, int64_t T, int64_t k, int64_t H, int64_t step, int64_t rows, const int32_t* positions) {
+    if (T < 0 || k < 0 || H < 0 || rows < 0) return fail(BSQ_ERR_SHAPE, "%s: negative size", fn);
+    if (H % step != 0) return fail(BSQ_ERR_SHAPE, "%s: the width (%lld) must be a multiple of %lld", fn, (long long)H, (long long)step);
+    if (T > (int64_t)1 << 23 || H > (int64_t)1 << 24 || T * ((H + 511) / 512) > (int64_t)1 << 25)
+        return fail(BSQ_ERR_SHAPE, "%s: %lld tokens of width %lld are too many for one launch", fn, (long long)T, (long long)H);
+    if (k > 64) return fail(BSQ_ERR_SHAPE, "%s: k (%lld) must be at most 64", fn, (long long)k);
+    if (rows > 0x7FFFFFFF) return fail(BSQ_ERR_SHAPE, "%s: %lld rows exceed 2^31 - 1", fn, (long long)rows);
+    if (T * k > 0 && !positions) return fail(BSQ_ERR_NULL, "%s: positions is NULL", fn);
+    if (unaligned(positions, 4)) return fail(BSQ_ERR_ALIGN, "%s: positions is not aligned", fn);
+    return BSQ_OK;
+}
+
+int gather_check(const char* fn, int64_t T, int64_t k, int64_t H, int64_t step, const void* x, int64_t ldx,
+                 const int32_t* positions, const int32_t* source, int64_t rows, const void* out, const void* scales) {
+    const int st = slots_check(fn, T, k, H, step, rows, positions);
+    if (st) return st;
+    if (rows == 0 || H == 0) return BSQ_OK;
+    if (T > 0 && !x) return fail(BSQ_ERR_NULL, "%s: x is NULL", fn);
+    if (T > 1 && (ldx < H || ldx % 8 != 0))
+        return fail(BSQ_ERR_SHAPE, "%s: ldx (%lld) must be a multiple of 8 and at least the width", fn, (long long)ldx);
+    if (!source || !out || !scales) return fail(BSQ_ERR_NULL, "%s: source or an output is NULL", fn);
+    if (misaligned(x) || misaligned(out) || misaligned(scales) || unaligned(source, 4))
+        return fail(BSQ_ERR_ALIGN, "%s: a pointer is not aligned", fn);
+    return BSQ_OK;
+}
+
+bool bad_type(int t) { return t != BSQ_OUT_BF16 && t != BSQ_OUT_F32; }
+
+}  // namespace
+
+extern "C" {
+
+int64_t moe_sort_rows(int64_t slots, int64_t experts, int64_t align) {
+    return sort_sizes_check("moe_sort_rows", slots, experts, align) ? -1 : sorted_rows(slots, experts, align);
+}
+
+int64_t moe_sort_workspace_bytes(int64_t slots, int64_t experts) {
+    if (sort_sizes_check("moe_sort_workspace_bytes", slots, experts, 1)) return -1;
+    return bsq::moe_sort_counts(slots, experts) * 4;
+}
+
+int moe_sort(const void* experts, int id_bytes, int64_t slots, int64_t num_experts, int64_t align, int64_t rows,
+             int64_t* offsets, int32_t* positions, int32_t* source, void* workspace, void* hip_stream) {
+    static const char* fn = "moe_sort";
+    if (id_bytes != 4 && id_bytes != 8) return fail(BSQ_ERR_ARG, "%s: id_bytes must be 4 or 8, got %d", fn, id_bytes);
+    const int st = sort_sizes_check(fn, slots, num_experts, align);
+    if (st) return st;
+    if (rows < sorted_rows(slots, num_experts, align) || rows > 0x7FFFFFFF)
+        return fail(BSQ_ERR_SHAPE, "%s: rows (%lld) must be in [%lld, 2^31)", fn, (long long)rows,
+                    (long long)sorted_rows(slots, num_experts, align));
+    if (!offsets || !workspace || (slots > 0 && (!experts || !positions)) || (rows > 0 && !source))
+        return fail(BSQ_ERR_NULL, "%s: NULL argument", fn);
+    if (unaligned(offsets, 8) || misaligned(workspace) || unaligned(experts, (uintptr_t)id_bytes) || unaligned(positions, 4) ||
+        unaligned(source, 4))
+        return fail(BSQ_ERR_ALIGN, "%s: a pointer is not aligned", fn);
+    return launched(bsq::launch_moe_sort(experts, id_bytes == 8, slots, num_experts, align, rows, offsets, positions, source,
+                                         static_cast<int32_t*>(workspace), hip_stream), fn);
+}
+
+int moe_gather(int64_t tokens, int64_t k, int64_t width, const void* x, int64_t ldx, const int32_t* positions,
+               const int32_t* source, int64_t rows, void* out, void* hip_stream) {
+    static const char* fn = "moe_gather";
+    const int st = gather_check(fn, tokens, k, width, 8, x, ldx, positions, source, rows, out, out);
+    if (st) return st;
+    return launched(bsq::launch_moe_gather(x, ldx, tokens, k, width, positions, source, rows, out, hip_stream), fn);
+}
+
+int moe_gather_nvfp4_rowscaled(int64_t tokens, int64_t k, int64_t width, const void* x, int64_t ldx,
+                               const int32_t* positions, const int32_t* source, int64_t rows, uint8_t* codes,
+                               uint8_t* scales, float* s_enc_rows, void* hip_stream) {
+    static const char* fn = "moe_gather_nvfp4_rowscaled";
+    const int st = gather_check(fn, tokens, k, width, 16, x, ldx, positions, source, rows, codes, scales);
+    if (st) return st;
+    if (rows == 0 || width == 0) return ok();
+    if (!s_enc_rows) return fail(BSQ_ERR_NULL, "%s: s_enc_rows is NULL", fn);
+    if (unaligned(s_enc_rows, 4)) return fail(BSQ_ERR_ALIGN, "%s: s_enc_rows is not aligned", fn);
+    return launched(bsq::launch_moe_gather_nvfp4(x, ldx, tokens, k, width, positions, source, rows, codes, scales,
+                                                 s_enc_rows, hip_stream), fn);
+}
+
+int moe_gather_mxfp8(int64_t tokens, int64_t k, int64_t width, const void* x, int64_t ldx, const int32_t* positions,
+                     const int32_t* source, int64_t rows, uint8_t* row_codes, uint8_t* row_scales, void* hip_stream) {
+    static const char* fn = "moe_gather_mxfp8";
+    const int st = gather_check(fn, tokens, k, width, 32, x, ldx, positions, source, rows, row_codes, row_scales);
+    if (st) return st;
+    return launched(bsq::launch_moe_gather_mxfp8(x, ldx, tokens, k, width, positions, source, rows, row_codes, row_scales,
+                                                 hip_stream), fn);
+}
+
+int moe_combine(int64_t tokens, int64_t k, int64_t width, const void* y, int y_dtype, int64_t rows,
+                const int32_t* positions, const float* weights, void* out, int out_dtype, void* hip_stream) {
+    static const char* fn = "moe_combine";
+    if (bad_type(y_dtype) || bad_type(out_dtype)) return fail(BSQ_ERR_ARG, "%s: a type must be 0 (bf16) or 1 (f32)", fn);
+    const int st = slots_check(fn, tokens, k, width, 8, rows, positions);
+    if (st) return st;
+    if (tokens == 0 || width == 0) return ok();
+    if (!out || (rows > 0 && k > 0 && !y)) return fail(BSQ_ERR_NULL, "%s: y or out is NULL", fn);
+    if (misaligned(out) || misaligned(y) || unaligned(weights, 4)) return fail(BSQ_ERR_ALIGN, "%s: a pointer is not aligned", fn);
+    return launched(bsq::launch_moe_combine(y, y_dtype == BSQ_OUT_F32, tokens, k, width, positions, rows, weights, out,
+                                            out_dtype == BSQ_OUT_F32, hip_stream), fn);
+}
+
+int moe_combine_backward(int64_t tokens, int64_t k, int64_t width, const void* dout, const void* y, int y_dtype,
+                         int64_t rows, const int32_t* positions, const int32_t* source, const float* weights, void* dy,
+                         float* dweights, void* hip_stream) {
+    static const char* fn = "moe_combine_backward";
+    if (bad_type(y_dtype)) return fail(BSQ_ERR_ARG, "%s: y_dtype must be 0 (bf16) or 1 (f32), got %d", fn, y_dtype);
+    const int st = slots_check(fn, tokens, k, width, 8, rows, positions);
+    if (st) return st;
+    const bool elems = rows > 0 && width > 0;
+    if (tokens * k > 0 && (!weights || !dweights || (width > 0 && !dout))) return fail(BSQ_ERR_NULL, "%s: NULL argument", fn);
+    if (elems && (!y || !dy || !source)) return fail(BSQ_ERR_NULL, "%s: NULL argument", fn);
+    if (misaligned(dout) || misaligned(y) || misaligned(dy) || unaligned(source, 4) || unaligned(weights, 4) ||
+        unaligned(dweights, 4))
+        return fail(BSQ_ERR_ALIGN, "%s: a pointer is not aligned", fn);
+    if (tokens * k == 0 && !elems) return ok();
+    return launched(bsq::launch_moe_combine_backward(dout, y, y_dtype == BSQ_OUT_F32, tokens, k, width, positions, source,
+                                                     elems ? rows : 0, weights, dy, dweights, hip_stream), fn);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- low-rank adapters
+
+namespace {
+
+int lora_check(const char* fn, int64_t M, int64_t N, int64_t K, int64_t r, int64_t L, const int32_t* adapters,
+               const void* lora_a, const void* lora_b, const float* scales, const void* workspace) {
+    if (L < 0 || L > (int64_t)1 << 24) return fail(BSQ_ERR_SHAPE, "%s: %lld adapters are not in [0, 2^24]", fn, (long long)L);
+    if (r < 8 || r > 256 || r % 8 != 0) return fail(BSQ_ERR_SHAPE, "%s: the rank (%lld) must be a multiple of 8 in [8, 256]", fn, (long long)r);
+    if (M == 0 || N == 0) return BSQ_OK;
+    if (!adapters || !workspace || (L > 0 && (!lora_b || (K > 0 && !lora_a)))) return fail(BSQ_ERR_NULL, "%s: NULL argument", fn);
+    if (misaligned(lora_a) || misaligned(lora_b) || misaligned(workspace) || unaligned(adapters, 4) || unaligned(scales, 4))
+        return fail(BSQ_ERR_ALIGN, "%s: a pointer is not aligned", fn);
+    return BSQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t lora_workspace_bytes(int64_t tokens, int64_t rank) {
+    if (tokens < 0 || tokens > (int64_t)1 << 20 || rank < 8 || rank > 256 || rank % 8 != 0) return -1;
+    return tokens * rank * 4;
+}
+
+int lora_add(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t num_adapters, const void* x, int64_t ldx,
+             const int32_t* adapters, const void* lora_a, const void* lora_b, const float* scales, const void* y, int64_t ldy,
+             void* out, int64_t ldo, int y_dtype, void* workspace, void* hip_stream) {
+    static const char* fn = "lora_add";
+    if (bad_type(y_dtype)) return fail(BSQ_ERR_ARG, "%s: y_dtype must be 0 (bf16) or 1 (f32), got %d", fn, y_dtype);
+    if (M < 0 || N < 0 || K < 0) return fail(BSQ_ERR_SHAPE, "%s: negative size", fn);
+    if (K % 8 != 0 || K >= gemm_k_limit(BSQ_FMT_NVFP4))
+        return fail(BSQ_ERR_SHAPE, "%s: K (%lld) must be a multiple of 8 below 2^24", fn, (long long)K);
+    if (M > (int64_t)1 << 20 || N > (int64_t)1 << 27 || bsq::lora_up_groups(M, N) >= (int64_t)1 << 24)
+        return fail(BSQ_ERR_SHAPE, "%s: %lld tokens by %lld are too large for one launch", fn, (long long)M, (long long)N);
+    const int st = lora_check(fn, M, N, K, rank, num_adapters, adapters, lora_a, lora_b, scales, workspace);
+    if (st) return st;
+    if (M == 0 || N == 0) return ok();
+    if (!y || !out || (K > 0 && !x)) return fail(BSQ_ERR_NULL, "%s: x, y or out is NULL", fn);
+    if (M > 1 && K > 0 && (ldx < K || ldx % 8 != 0))
+        return fail(BSQ_ERR_SHAPE, "%s: ldx (%lld) must be a multiple of 8 and at least K", fn, (long long)ldx);
+    if (M > 1 && (ldy < N || ldo < N)) return fail(BSQ_ERR_SHAPE, "%s: ldy and ldo must be at least N", fn);
+    if (out == y && M > 1 && ldo != ldy) return fail(BSQ_ERR_ARG, "%s: in place, ldo must be ldy", fn);
+    const uintptr_t item = y_dtype == BSQ_OUT_F32 ? 4 : 2;
+    if (misaligned(x) || unaligned(y, item) || unaligned(out, item)) return fail(BSQ_ERR_ALIGN, "%s: a pointer is not aligned", fn);
+    return launched(bsq::launch_lora_add(y_dtype == BSQ_OUT_F32, M, N, K, rank, num_adapters, x, ldx, adapters, lora_a, lora_b,
+                                         scales, y, ldy, out, ldo, static_cast<float*>(workspace), hip_stream), fn);
+}
+
+int nvfp4_lora_matvec(int flags, int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const uint8_t* w_codes,
+                      const uint8_t* w_scales, const float* w_s_enc, int64_t rank, int64_t num_adapters,
+                      const int32_t* adapters, const void* lora_a, const void* lora_b, const float* scales, void* y,
+                      int y_dtype, void* workspace, void* hip_stream) {
+    static const char* fn = "nvfp4_lora_matvec";
+    if (bad_type(y_dtype)) return fail(BSQ_ERR_ARG, "%s: y_dtype must be 0 (bf16) or 1 (f32), got %d", fn, y_dtype);
+    int st = matvec_check(fn, flags, M, N, K, x, ldx, w_codes, w_scales, w_s_enc, y);
+    if (st) return st;
+    st = lora_check(fn, M, N, K, rank, num_adapters, adapters, lora_a, lora_b, scales, workspace);
+    if (st) return st;
+    return launched(bsq::launch_nvfp4_lora_matvec(x, ldx, M, N, K, w_codes, w_scales, w_s_enc, flags != 0, rank, num_adapters,
+                                                  adapters, lora_a, lora_b, scales, static_cast<float*>(workspace), y,
+                                                  y_dtype == BSQ_OUT_F32, hip_stream), fn);
+}
+
+}  // extern "C"

@@ -68,6 +68,30 @@ int launch_grad_clip(const void* const* grads, void* const* outs, const int64_t*
                      int64_t count, const double* sumsq, double max_norm, float* norm, void* hip_stream);
 int launch_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes,
                           int64_t count, double max_norm, float* norm, double* workspace, void* hip_stream);
+int64_t moe_sort_counts(int64_t n, int64_t E);   // int32 of the workspace
+int launch_moe_sort(const void* experts, int id8, int64_t n, int64_t E, int64_t align, int64_t rows, int64_t* offsets,
+                    int32_t* positions, int32_t* source, int32_t* counts, void* hip_stream);
+int launch_moe_gather(const void* x, int64_t ldx, int64_t T, int64_t k, int64_t H, const int32_t* positions,
+                      const int32_t* source, int64_t rows, void* out, void* hip_stream);
+int launch_moe_gather_mxfp8(const void* x, int64_t ldx, int64_t T, int64_t k, int64_t H, const int32_t* positions,
+                            const int32_t* source, int64_t rows, uint8_t* codes, uint8_t* scales, void* hip_stream);
+int launch_moe_gather_nvfp4(const void* x, int64_t ldx, int64_t T, int64_t k, int64_t H, const int32_t* positions,
+                            const int32_t* source, int64_t rows, uint8_t* codes, uint8_t* scales, float* s_enc,
+                            void* hip_stream);
+int launch_moe_combine(const void* y, int y_f32, int64_t T, int64_t k, int64_t H, const int32_t* positions, int64_t rows,
+                       const float* weights, void* out, int out_f32, void* hip_stream);
+int launch_moe_combine_backward(const void* dout, const void* y, int y_f32, int64_t T, int64_t k, int64_t H,
+                                const int32_t* positions, const int32_t* source, int64_t rows, const float* weights,
+                                void* dy, float* dweights, void* hip_stream);
+// workgroups of the up products' launch; 256 threads each, below 2^32 in all
+int64_t lora_up_groups(int64_t M, int64_t N);
+int launch_lora_add(int f32, int64_t M, int64_t N, int64_t K, int64_t r, int64_t L, const void* x, int64_t ldx,
+                    const int32_t* adapters, const void* lora_a, const void* lora_b, const float* scales, const void* y,
+                    int64_t ldy, void* out, int64_t ldo, float* workspace, void* hip_stream);
+int launch_nvfp4_lora_matvec(const void* x, int64_t ldx, int64_t M, int64_t N, int64_t K, const uint8_t* w_codes,
+                             const uint8_t* w_scales, const float* w_s_enc, int rows, int64_t r, int64_t L,
+                             const int32_t* adapters, const void* lora_a, const void* lora_b, const float* scales,
+                             float* workspace, void* y, int y_f32, void* hip_stream);
 const char* hip_error_string(int e);
 
 }  // namespace bsq

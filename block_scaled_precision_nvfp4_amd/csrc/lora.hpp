@@ -1,0 +1,70 @@
+// lora.hpp -- what the adapters' kernels (lora.hip) and the product of tokens with NVFP4 weights (matvec.hip) share.
+#pragma once
+
+#include "device_common.hpp"
+
+namespace bsq {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+
+struct LoraArgs {
+    int64_t M, N, K;
+    int r;                      // a multiple of 8
+    int64_t L;                  // adapters
+    const uint16_t* x;
+    int64_t ldx;
+    const int32_t* adapters;    // [M]; outside [0, L): none
+    const uint16_t* a;          // [L][r][K]
+    const uint16_t* b;          // [L][N][r]
+    const float* scales;        // [L], or none
+    float* t;                   // [M][r]: the down products
+    const void* y;
+    int64_t ldy;
+    void* out;
+    int64_t ldo;
+};
+
+int launch_lora_down(const LoraArgs& a, hipStream_t s);
+
+// Eight values as three bf16 parts that add up to each exactly (8 bits of the significand each, cut, not
+// rounded, so that a large value does not become infinite).  An infinity or NaN goes into the first part alone.
+__device__ __forceinline__ void lora_split8(const float* t, bf16x8_t (&part)[3]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float v = t[i];
+        const uint32_t u = __float_as_uint(v);
+        const bool fin = (u & 0x7F800000u) != 0x7F800000u;
+        const uint32_t hi = (u & 0xFFFF0000u) | (!fin && (u & 0x7FFFFFu) ? 0x400000u : 0u);
+        const float r1 = v - __uint_as_float(hi);
+        const uint32_t mid = __float_as_uint(r1) & 0xFFFF0000u;
+        const float r2 = r1 - __uint_as_float(mid);
+        part[0][i] = __builtin_bit_cast(__bf16, (uint16_t)(hi >> 16));
+        part[1][i] = __builtin_bit_cast(__bf16, (uint16_t)(fin ? mid >> 16 : 0u));
+        part[2][i] = __builtin_bit_cast(__bf16, (uint16_t)(fin ? __float_as_uint(r2) >> 16 : 0u));
+    }
+}
+
+// y + s_a sum_q t[m][q] B_a[n][q] of token m's adapter a, in fp32; y where it has none.
+__device__ __forceinline__ float lora_added(const LoraArgs& a, int64_t m, int64_t n, float y) {
+    const int id = a.adapters[m];
+    if (id < 0 || id >= a.L) return y;
+    const uint16_t* b = a.b + ((int64_t)id * a.N + n) * a.r;
+    const float* t = a.t + m * a.r;
+    float s = 0.0f;
+    for (int q = 0; q < a.r; q += 8) {
+        float w[8];
+        unpack_bf16x8(*(const uint4*)(b + q), w);
+        const float4 t0 = *(const float4*)(t + q), t1 = *(const float4*)(t + q + 4);
+        s = __builtin_fmaf(t0.x, w[0], s);
+        s = __builtin_fmaf(t0.y, w[1], s);
+        s = __builtin_fmaf(t0.z, w[2], s);
+        s = __builtin_fmaf(t0.w, w[3], s);
+        s = __builtin_fmaf(t1.x, w[4], s);
+        s = __builtin_fmaf(t1.y, w[5], s);
+        s = __builtin_fmaf(t1.z, w[6], s);
+        s = __builtin_fmaf(t1.w, w[7], s);
+    }
+    return __builtin_fmaf(a.scales ? a.scales[id] : 1.0f, s, y);
+}
+
+}  // namespace bsq

@@ -25,10 +25,10 @@
 // 132 KiB of LDS from 16 on) that meets at a barrier after every chunk.
 #include "activation.hpp"
 #include "launch.hpp"
+#include "lora.hpp"
 
 namespace bsq {
 
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx2 __attribute__((ext_vector_type(2)));
 
@@ -52,6 +52,7 @@ struct MvArgs {
     int y_f32;
     int act;
     int wr;               // 16-row blocks of a workgroup; its waves are wr times as many as parts of K
+    LoraArgs lora;        // the tokens' adapters, for the kernels that add their products
 };
 
 // One lane's 64 elements of a weight row: their codes and the bytes of their 4 block scales.
@@ -156,7 +157,7 @@ __device__ __forceinline__ uint32_t mv_word(const MvPiece& p) {
 
 // The workgroup's outputs from the sums of its parts of K.  sum(o, q, b, m, n): operand o's sum of part q,
 // row block b, token m, row n of the block.  s0: the tensor scales of this thread's first output.
-template <bool GATED, class S>
+template <bool GATED, bool LORA, class S>
 __device__ __forceinline__ void mv_join(const MvArgs& a, int parts, int tokens, int64_t m0,
                                         const float (&s0)[GATED ? 2 : 1], S&& sum) {
     constexpr int NW = GATED ? 2 : 1;
@@ -174,6 +175,7 @@ __device__ __forceinline__ void mv_join(const MvArgs& a, int parts, int tokens, 
         float y = v[0];
         if constexpr (GATED)
             y = (a.act == 0 ? act_value<0>(v[0]) : a.act == 1 ? act_value<1>(v[0]) : act_value<2>(v[0])) * v[NW - 1];
+        if constexpr (LORA) y = lora_added(a.lora, m, n, y);
         if (a.y_f32) ((float*)a.y)[m * a.N + n] = y;
         else ((uint16_t*)a.y)[m * a.N + n] = (uint16_t)bf16x2_rne(y, 0.0f);
     }
@@ -245,7 +247,7 @@ __device__ __forceinline__ void mv_use_one(const MvPiece (&p)[NW], const MvOneX&
 constexpr int MV_ONE_WAVES = 16;
 
 // A workgroup: one token (blockIdx.y) by 16 weight rows, K dealt in chunks to its waves.
-template <bool GATED, int LOAD>
+template <bool GATED, int LOAD, bool LORA>
 __global__ __launch_bounds__(64 * MV_ONE_WAVES) void matvec_kernel(MvArgs a) {
     constexpr int NW = GATED ? 2 : 1, D = 4 / NW;   // chunks in flight
     __shared__ float red[MV_ONE_WAVES][NW][4][MV_ROWS + 1];
@@ -312,7 +314,7 @@ __global__ __launch_bounds__(64 * MV_ONE_WAVES) void matvec_kernel(MvArgs a) {
 #pragma unroll
     for (int o = 0; o < NW; ++o) red[wave][o][g][r16] = (acc[o][0] + acc[o][1]) + (acc[o][2] + acc[o][3]);
     __syncthreads();
-    mv_join<GATED>(a, parts, 1, m0, s0, [&](int o, int q, int, int, int n) {
+    mv_join<GATED, LORA>(a, parts, 1, m0, s0, [&](int o, int q, int, int, int n) {
         const float (&f)[4][MV_ROWS + 1] = red[q][o];
         return (f[0][n] + f[1][n]) + (f[2][n] + f[3][n]);
     });
@@ -330,7 +332,7 @@ constexpr int mv_parts(int t) { return t == 4 ? 16 : 128 / t; }   // at most
 constexpr int mv_waves(int t) { return t == 4 ? 16 : 8; }        // at most
 constexpr int mv_min_wr(int t) { return t <= 16 ? 1 : t / 16; }   // so that a thread carries T / 2 wr <= 8 vectors
 
-template <int T, bool GATED, int LOAD>
+template <int T, bool GATED, int LOAD, bool LORA>
 __global__ __launch_bounds__(64 * mv_waves(T)) void matvec_tokens_kernel(MvArgs a) {
     constexpr int NW = GATED ? 2 : 1, MT = (T + 15) / 16, XV = T == 4 ? 2 : 8, RS = MV_ROWS + 1;
     constexpr int XBUF = mv_parts(T) * T * MV_XPITCH;
@@ -435,7 +437,7 @@ __global__ __launch_bounds__(64 * mv_waves(T)) void matvec_tokens_kernel(MvArgs 
                 if (m < tokens) red[((wave * NW + o) * T + m) * RS + r16] = acc[o][t][r];
             }
     __syncthreads();
-    mv_join<GATED>(a, parts, tokens, m0, s0, [&](int o, int q, int b, int m, int n) {
+    mv_join<GATED, LORA>(a, parts, tokens, m0, s0, [&](int o, int q, int b, int m, int n) {
         return red[(((q * a.wr + b) * NW + o) * T + m) * RS + n];
     });
 }
@@ -444,14 +446,14 @@ __global__ __launch_bounds__(64 * mv_waves(T)) void matvec_tokens_kernel(MvArgs 
 
 // One token: as many waves share K as let every workgroup be resident at once (16 waves on each CU), at least
 // 4 and no more than there are chunks.
-template <bool GATED, int LOAD>
+template <bool GATED, int LOAD, bool LORA>
 static int launch_one(MvArgs a, hipStream_t s) {
     const int64_t blocks = (a.N + MV_ROWS - 1) / MV_ROWS, chunks = (a.K + MV_CHUNK - 1) / MV_CHUNK;
     int parts = MV_ONE_WAVES;
     while (parts > 4 && parts * blocks * a.M > MV_CUS * MV_ONE_WAVES) parts /= 2;
     while (parts > 1 && parts / 2 >= chunks) parts /= 2;
     a.wr = 1;
-    hipLaunchKernelGGL((matvec_kernel<GATED, LOAD>), dim3((unsigned)blocks, (unsigned)a.M), dim3(64 * parts), 0, s, a);
+    hipLaunchKernelGGL((matvec_kernel<GATED, LOAD, LORA>), dim3((unsigned)blocks, (unsigned)a.M), dim3(64 * parts), 0, s, a);
     return (int)hipGetLastError();
 }
 
@@ -462,7 +464,7 @@ static int64_t tokens_workgroups(const MvArgs& a) {
     return ((a.N + MV_ROWS * mv_min_wr(T) - 1) / (MV_ROWS * mv_min_wr(T))) * ((a.M + T - 1) / T);
 }
 
-template <int T, bool GATED, int LOAD>
+template <int T, bool GATED, int LOAD, bool LORA>
 static int launch_tokens(MvArgs a, hipStream_t s) {
     const int64_t blocks = (a.N + MV_ROWS - 1) / MV_ROWS, mb = (a.M + T - 1) / T;
     const int64_t chunks = (a.K + MV_CHUNK - 1) / MV_CHUNK;
@@ -470,7 +472,7 @@ static int launch_tokens(MvArgs a, hipStream_t s) {
     while (a.wr < 4 && a.wr * MV_CUS < blocks * mb) a.wr *= 2;
     int parts = mv_waves(T) / a.wr < mv_parts(T) ? mv_waves(T) / a.wr : mv_parts(T);
     while (parts > 1 && parts / 2 >= chunks) parts /= 2;
-    hipLaunchKernelGGL((matvec_tokens_kernel<T, GATED, LOAD>), dim3((unsigned)((blocks + a.wr - 1) / a.wr), (unsigned)mb),
+    hipLaunchKernelGGL((matvec_tokens_kernel<T, GATED, LOAD, LORA>), dim3((unsigned)((blocks + a.wr - 1) / a.wr), (unsigned)mb),
                        dim3(64 * a.wr * parts), 0, s, a);
     return (int)hipGetLastError();
 }
@@ -480,13 +482,20 @@ static int launch_tokens(MvArgs a, hipStream_t s) {
 // 64 x 14336 x 8192 gated 142 / 88 / 61, 64 x 14336 x 4096 54 / 34 / 25; 64 x 6151 x 4112 31 / 21 / 28, 64 x
 // 4096 x 4096 15 / 13 / 24, 32 x 14336 x 4096 28 / 19 / 21; 32 x 4096 x 4096 11 / 13 / 20, 33 x 1000 x
 // 16384 17 / 31 / 63.
-template <bool GATED, int LOAD>
+template <bool GATED, int LOAD, bool LORA>
 static int launch_mv(const MvArgs& a, hipStream_t s) {
-    if (a.M == 1) return launch_one<GATED, LOAD>(a, s);
-    if (a.M <= 4) return launch_tokens<4, GATED, LOAD>(a, s);
-    if (a.M > 4096 || (a.M > 32 && 4 * tokens_workgroups<64>(a) >= 3 * MV_CUS)) return launch_tokens<64, GATED, LOAD>(a, s);
-    if (a.M > 16 && 4 * tokens_workgroups<32>(a) >= 3 * MV_CUS) return launch_tokens<32, GATED, LOAD>(a, s);
-    return launch_tokens<16, GATED, LOAD>(a, s);
+    if (a.M == 1) return launch_one<GATED, LOAD, LORA>(a, s);
+    if (a.M <= 4) return launch_tokens<4, GATED, LOAD, LORA>(a, s);
+    if (a.M > 4096 || (a.M > 32 && 4 * tokens_workgroups<64>(a) >= 3 * MV_CUS)) return launch_tokens<64, GATED, LOAD, LORA>(a, s);
+    if (a.M > 16 && 4 * tokens_workgroups<32>(a) >= 3 * MV_CUS) return launch_tokens<32, GATED, LOAD, LORA>(a, s);
+    return launch_tokens<16, GATED, LOAD, LORA>(a, s);
+}
+
+template <bool GATED, bool LORA>
+static int launch_any(const MvArgs& a, hipStream_t s) {
+    if (a.K < 64) return launch_tokens<64, GATED, MV_BLOCKS, LORA>(a, s);
+    if (a.K % 64 == 0) return launch_mv<GATED, MV_ALIGNED, LORA>(a, s);
+    return launch_mv<GATED, MV_SHIFTED, LORA>(a, s);
 }
 
 int launch_nvfp4_matvec(int act, const void* x, int64_t ldx, int64_t M, int64_t N, int64_t K, const uint8_t* w_codes,
@@ -495,11 +504,22 @@ int launch_nvfp4_matvec(int act, const void* x, int64_t ldx, int64_t M, int64_t 
                         void* hip_stream) {
     if (M == 0 || N == 0) return 0;
     const MvArgs a{(const uint16_t*)x, ldx, M, N, K, {{w_codes, w_scales, w_s_enc}, {up_codes, up_scales, up_s_enc}},
-                   rows, y, y_f32, act, 1};
+                   rows, y, y_f32, act, 1, {}};
     hipStream_t s = (hipStream_t)hip_stream;
-    if (K < 64) return act < 0 ? launch_tokens<64, false, MV_BLOCKS>(a, s) : launch_tokens<64, true, MV_BLOCKS>(a, s);
-    if (K % 64 == 0) return act < 0 ? launch_mv<false, MV_ALIGNED>(a, s) : launch_mv<true, MV_ALIGNED>(a, s);
-    return act < 0 ? launch_mv<false, MV_SHIFTED>(a, s) : launch_mv<true, MV_SHIFTED>(a, s);
+    return act < 0 ? launch_any<false, false>(a, s) : launch_any<true, false>(a, s);
+}
+
+int launch_nvfp4_lora_matvec(const void* x, int64_t ldx, int64_t M, int64_t N, int64_t K, const uint8_t* w_codes,
+                             const uint8_t* w_scales, const float* w_s_enc, int rows, int64_t r, int64_t L,
+                             const int32_t* adapters, const void* lora_a, const void* lora_b, const float* scales,
+                             float* workspace, void* y, int y_f32, void* hip_stream) {
+    if (M == 0 || N == 0) return 0;
+    hipStream_t s = (hipStream_t)hip_stream;
+    MvArgs a{(const uint16_t*)x, ldx, M, N, K, {{w_codes, w_scales, w_s_enc}, {}}, rows, y, y_f32, -1, 1, {}};
+    a.lora = LoraArgs{M, N, K, (int)r, L, a.x, ldx, adapters, (const uint16_t*)lora_a, (const uint16_t*)lora_b, scales,
+                      workspace, y, N, y, N};
+    const int e = launch_lora_down(a.lora, s);
+    return e ? e : launch_any<false, true>(a, s);
 }
 
 }  // namespace bsq

@@ -1,0 +1,590 @@
+// moe.hip -- the way of tokens to their experts and back.  A token has k slots, slot i = t k + j being its
+// j-th expert's:
+//
+//   sort      c_g slots want expert g; group g starts at a multiple of `align`, and a slot's row is its group's start
+//             plus the slots before it that want the same expert (a stable counting sort)
+//   gather    out[row of slot i] = x[i / k], as bf16, row-scaled NVFP4 or MXFP8; rows of no slot are zero
+//   combine   out[t] = sum_j w[t][j] y[row of slot t k + j]
+//   backward  dy[row of slot i] = w_i dout[i / k],  dw_i = <dout[i / k], y[row of slot i]>
+//
+// None of them does arithmetic to speak of: a call is bound by the bytes of its rows, or by latency.
+#include "encode.hpp"
+#include "launch.hpp"
+
+namespace bsq {
+
+// ---------------------------------------------------------------- sort
+
+constexpr int SORT_WAVES = 16, SORT_THREADS = 64 * SORT_WAVES;
+constexpr int SORT_HIST = 8192;        // counters of a workgroup: its waves' times the experts
+
+struct SortArgs {
+    const void* experts;   // ids of 4 or 8 bytes
+    int id8;
+    int64_t n;
+    int E;
+    int align;             // a power of two
+    int64_t rows;
+    int64_t* offsets;
+    int32_t* positions;
+    int32_t* source;
+    int32_t* counts;       // [workgroups][E], with several workgroups
+    int64_t chunk;         // slots of a workgroup, a multiple of its threads
+};
+
+// A slot's expert, E for one that is dropped.
+__device__ __forceinline__ int sort_id(const SortArgs& a, int64_t i) {
+    const int64_t id = a.id8 ? ((const int64_t*)a.experts)[i] : (int64_t)((const int32_t*)a.experts)[i];
+    return id >= 0 && id < a.E ? (int)id : a.E;
+}
+
+// The lanes of the wave whose id (of `bits` bits) is this lane's.
+__device__ __forceinline__ uint64_t same_id(int id, int bits) {
+    uint64_t m = ~0ull;
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t one = __ballot((id >> b) & 1);
+        m &= ((id >> b) & 1) ? one : ~one;
+    }
+    return m;
+}
+
+__global__ __launch_bounds__(SORT_THREADS) void moe_count_kernel(SortArgs a) {
+    __shared__ int hist[1024];
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
+    __syncthreads();
+    const int bits = 32 - __builtin_clz(a.E);
+    const int64_t first = (int64_t)blockIdx.x * a.chunk;
+    for (int64_t c = 0; c < a.chunk; c += blockDim.x) {
+        const int64_t i = first + c + threadIdx.x;
+        const int id = i < a.n ? sort_id(a, i) : a.E;
+        const uint64_t m = same_id(id, bits);
+        if (id < a.E && (int)(threadIdx.x & 63) == __builtin_ctzll(m)) atomicAdd(&hist[id], __popcll(m));
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
+}
+
+// A workgroup places its chunk of slots: counts of its waves, the slots before it (from the other workgroups'
+// counts), the groups' starts, and then every slot's rank among those of its wave.
+__global__ __launch_bounds__(SORT_THREADS) void moe_place_kernel(SortArgs a) {
+    __shared__ int next[SORT_HIST];                    // [wave][E]: the wave's count, then its next row, of each expert
+    __shared__ int start[1024], total[1024], before[1024];
+    __shared__ int sums[SORT_WAVES];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, E = a.E;
+    const int bits = 32 - __builtin_clz(E);
+    const int64_t mine = a.chunk / waves;              // slots of a wave, one after another
+    const int64_t first = (int64_t)blockIdx.x * a.chunk + wave * mine;
+    for (int i = threadIdx.x; i < waves * E; i += blockDim.x) next[i] = 0;
+    __syncthreads();
+    for (int64_t c = 0; c < mine; c += 64) {
+        const int64_t i = first + c + lane;
+        const int id = i < a.n ? sort_id(a, i) : E;
+        const uint64_t m = same_id(id, bits);
+        if (id < E && lane == __builtin_ctzll(m)) atomicAdd(&next[wave * E + id], __popcll(m));
+    }
+    __syncthreads();
+    // slots of each expert in all, and before this workgroup
+    if (gridDim.x == 1) {
+        for (int e = threadIdx.x; e < E; e += blockDim.x) {
+            int s = 0;
+            for (int w = 0; w < waves; ++w) s += next[w * E + e];
+            total[e] = s;
+            before[e] = 0;
+        }
+    } else {
+        for (int e = threadIdx.x; e < E; e += blockDim.x) {
+            int s = 0, b = 0;
+            for (int g = 0; g < (int)gridDim.x; ++g) {
+                const int v = a.counts[(int64_t)g * E + e];
+                s += v;
+                if (g < (int)blockIdx.x) b += v;
+            }
+            total[e] = s;
+            before[e] = b;
+        }
+    }
+    __syncthreads();
+    // the groups' starts: a running sum of the padded totals, a stretch of experts after another
+    int base = 0;
+    for (int e0 = 0; e0 < E; e0 += blockDim.x) {
+        const int e = e0 + threadIdx.x;
+        const int padded = e < E ? (total[e] + a.align - 1) & -a.align : 0;
+        int v = padded;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int u = __shfl_up(v, o);
+            if (lane >= o) v += u;
+        }
+        if (lane == 63) sums[wave] = v;
+        __syncthreads();
+        int at = base, all = 0;
+        for (int w = 0; w < waves; ++w) {
+            if (w < wave) at += sums[w];
+            all += sums[w];
+        }
+        if (e < E) start[e] = at + v - padded;
+        base += all;
+        __syncthreads();
+    }
+    if (blockIdx.x == 0) {
+        for (int e = threadIdx.x; e < E; e += blockDim.x) a.offsets[e] = start[e];
+        if (threadIdx.x == 0) a.offsets[E] = base;
+    }
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        int at = start[e] + before[e];
+        for (int w = 0; w < waves; ++w) {
+            const int c = next[w * E + e];
+            next[w * E + e] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+    for (int64_t c = 0; c < mine; c += 64) {
+        const int64_t i = first + c + lane;
+        const int id = i < a.n ? sort_id(a, i) : E;
+        const uint64_t m = same_id(id, bits);
+        const int leader = __builtin_ctzll(m);
+        int at = 0;
+        if (id < E && lane == leader) at = atomicAdd(&next[wave * E + id], __popcll(m));
+        at = __shfl(at, leader) + __popcll(m & ((1ull << lane) - 1));
+        if (i < a.n) {
+            a.positions[i] = id < E ? at : -1;
+            if (id < E) a.source[at] = (int32_t)i;
+        }
+    }
+    // rows of no slot: the groups' padding, and what lies behind the last group
+    for (int e = blockIdx.x + gridDim.x * wave; e < E; e += gridDim.x * waves) {
+        const int end = e + 1 < E ? start[e + 1] : base;
+        for (int r = start[e] + total[e] + lane; r < end; r += 64) a.source[r] = -1;
+    }
+    for (int64_t r = base + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < a.rows; r += (int64_t)gridDim.x * blockDim.x)
+        a.source[r] = -1;
+}
+
+static int64_t sort_groups(int64_t n, int64_t E, int64_t* chunk) {
+    const int64_t threads = E > SORT_HIST / SORT_WAVES ? SORT_HIST / E * 64 : SORT_THREADS;
+    int64_t c = 4096;
+    while ((n + c - 1) / c > 128) c *= 2;
+    *chunk = c < threads ? threads : c;
+    return n <= 16384 ? 1 : (n + *chunk - 1) / *chunk;
+}
+
+int64_t moe_sort_counts(int64_t n, int64_t E) {
+    int64_t chunk;
+    return sort_groups(n, E, &chunk) * E;
+}
+
+int launch_moe_sort(const void* experts, int id8, int64_t n, int64_t E, int64_t align, int64_t rows, int64_t* offsets,
+                    int32_t* positions, int32_t* source, int32_t* counts, void* hip_stream) {
+    hipStream_t s = (hipStream_t)hip_stream;
+    SortArgs a{experts, id8, n, (int)E, (int)align, rows, offsets, positions, source, counts, 0};
+    const int64_t groups = sort_groups(n, E, &a.chunk);
+    int waves = SORT_WAVES;
+    while (waves * E > SORT_HIST) waves /= 2;
+    if (groups == 1) a.chunk = (n + 64 * waves - 1) / (64 * waves) * (64 * waves);
+    if (groups > 1) {
+        hipLaunchKernelGGL(moe_count_kernel, dim3((unsigned)groups), dim3(64 * waves), 0, s, a);
+        const int e = (int)hipGetLastError();
+        if (e) return e;
+    }
+    hipLaunchKernelGGL(moe_place_kernel, dim3((unsigned)groups), dim3(64 * waves), 0, s, a);
+    return (int)hipGetLastError();
+}
+
+// ---------------------------------------------------------------- rows without a slot
+
+// Waves at the end of a launch write zeros to the rows that no slot fills.  Wave w of `waves` looks at the rows w,
+// w + waves, ..., 64 at a time, so that a long stretch of such rows (behind the last group) is shared by all.
+template <class F>
+__device__ __forceinline__ void for_empty_rows(const int32_t* source, int64_t rows, int64_t slots, int64_t wave,
+                                               int64_t waves, F&& zero) {
+    const int lane = threadIdx.x & 63;
+    for (int64_t r0 = wave; r0 < rows; r0 += 64 * waves) {
+        const int64_t r = r0 + lane * waves;
+        bool empty = false;
+        if (r < rows) {
+            const int32_t i = source[r];
+            empty = i < 0 || i >= slots;
+        }
+        for (uint64_t m = __ballot(empty); m != 0; m &= m - 1) zero(r0 + __builtin_ctzll(m) * waves);
+    }
+}
+
+// ---------------------------------------------------------------- gather
+
+constexpr int MOE_THREADS = 256, MOE_WAVES = MOE_THREADS / 64;
+
+struct MoeSlots {
+    const int32_t* positions;   // [T][k]
+    const int32_t* source;      // [rows]
+    int64_t T;
+    int k;
+    int64_t rows;
+    // slot j's row of token t, -1: none
+    __device__ __forceinline__ int64_t row(int64_t t, int j) const {
+        const int32_t p = positions[t * k + j];
+        return p >= 0 && p < rows ? p : -1;
+    }
+};
+
+struct GatherArgs {
+    const uint16_t* x;
+    int64_t ldx, H;
+    MoeSlots s;
+    unsigned token_groups;   // workgroups of the tokens; the others look for rows without a slot
+    void* out;               // bf16 rows, or codes
+    uint8_t* scales;
+    float* s_enc;
+};
+
+// A token's row is read once and written k times.  A wave takes 512 U elements of a token.
+template <int U>
+__global__ __launch_bounds__(MOE_THREADS) void moe_gather_kernel(GatherArgs a) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    uint16_t* out = (uint16_t*)a.out;
+    if (blockIdx.x >= a.token_groups) {
+        const int64_t w = (int64_t)(blockIdx.x - a.token_groups) * MOE_WAVES + wave;
+        for_empty_rows(a.s.source, a.s.rows, a.s.T * a.s.k, w, (int64_t)(gridDim.x - a.token_groups) * MOE_WAVES, [&](int64_t r) {
+            for (int64_t c = 8 * lane; c < a.H; c += 512) *(uint4*)(out + r * a.H + c) = make_uint4(0, 0, 0, 0);
+        });
+        return;
+    }
+    const int64_t pieces = (a.H + 512 * U - 1) / (512 * U);
+    const int64_t u = (int64_t)blockIdx.x * MOE_WAVES + wave, t = u / pieces, c0 = (u % pieces) * (512 * U) + 8 * lane;
+    if (t >= a.s.T) return;
+    uint4 v[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+        if (c0 + 512 * i < a.H) v[i] = load16_stream(a.x + t * a.ldx + c0 + 512 * i);
+    for (int j = 0; j < a.s.k; ++j) {
+        const int64_t r = a.s.row(t, j);
+        if (r < 0) continue;
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (c0 + 512 * i < a.H) *(uint4*)(out + r * a.H + c0 + 512 * i) = v[i];
+    }
+}
+
+static unsigned empty_groups(int64_t rows) {   // a wave for 64 rows, at most 1024 workgroups
+    const int64_t g = (rows + 64 * MOE_WAVES - 1) / (64 * MOE_WAVES);
+    return (unsigned)(g < 1 ? 1 : g > 1024 ? 1024 : g);
+}
+
+template <int U>
+static int launch_gather(GatherArgs a, hipStream_t s) {
+    const int64_t waves = a.s.T * ((a.H + 512 * U - 1) / (512 * U));
+    a.token_groups = (unsigned)((waves + MOE_WAVES - 1) / MOE_WAVES);
+    hipLaunchKernelGGL((moe_gather_kernel<U>), dim3(a.token_groups + empty_groups(a.s.rows)), dim3(MOE_THREADS), 0, s, a);
+    return (int)hipGetLastError();
+}
+
+int launch_moe_gather(const void* x, int64_t ldx, int64_t T, int64_t k, int64_t H, const int32_t* positions,
+                      const int32_t* source, int64_t rows, void* out, void* hip_stream) {
+    if (rows == 0 || H == 0) return 0;
+    return launch_gather<4>({(const uint16_t*)x, ldx, H, {positions, source, T, (int)k, rows}, 0, out, nullptr, nullptr},
+                            (hipStream_t)hip_stream);
+}
+
+__device__ __forceinline__ float max8(const float v[8]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = __builtin_fmaxf(m, __builtin_fabsf(v[e]));
+    return m;
+}
+
+// The MXFP8 codes and scale byte of a lane's 8 elements of a block of 32, which 4 lanes share.  Each block is encoded as
+// its own amax asks: a value that is not finite becomes NaN whatever the wave's other blocks hold.
+__device__ __forceinline__ void mx_row_unit(const uint4 q, uint2& w, uint32_t& sb) {
+    const uint32_t p[4] = {q.x, q.y, q.z, q.w};
+    const uint32_t M = mx_quad_amax(p);
+    const bool small = (M & 0xFFFFu) < MX_PACKED_LEAST;
+    mx_encode_packed(p, small ? 0x3F803F80u : M, w.x, w.y, sb);
+    if (__ballot(small) == 0) return;
+    float v[8];
+    unpack_bf16x8(q, v);
+    if (small) {   // the scale byte is 0: amax below 2^-118, zero among them
+        const float inv = mx_inv_scale(0);
+        w = make_uint2(e4m3_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                       e4m3_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+        if ((M & 0xFFFFu) == 0) w = make_uint2(0, 0);   // -0 among them
+        sb = 0;
+    }
+}
+
+// MXFP8: a token is cast once, and its codes and scales written k times.  A lane holds a quarter of a block of 32.
+template <int U>
+__global__ __launch_bounds__(MOE_THREADS) void moe_gather_mxfp8_kernel(GatherArgs a) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    uint8_t* codes = (uint8_t*)a.out;
+    const int64_t S = a.H / 32;
+    if (blockIdx.x >= a.token_groups) {
+        const int64_t w = (int64_t)(blockIdx.x - a.token_groups) * MOE_WAVES + wave;
+        for_empty_rows(a.s.source, a.s.rows, a.s.T * a.s.k, w, (int64_t)(gridDim.x - a.token_groups) * MOE_WAVES, [&](int64_t r) {
+            for (int64_t c = 16 * lane; c < a.H; c += 1024) *(uint4*)(codes + r * a.H + c) = make_uint4(0, 0, 0, 0);
+            for (int64_t b = lane; b < S; b += 64) a.scales[r * S + b] = 0;
+        });
+        return;
+    }
+    const int64_t pieces = (a.H + 512 * U - 1) / (512 * U);
+    const int64_t u = (int64_t)blockIdx.x * MOE_WAVES + wave, t = u / pieces, c0 = (u % pieces) * (512 * U) + 8 * lane;
+    if (t >= a.s.T) return;
+    uint4 q[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        q[i] = make_uint4(0, 0, 0, 0);
+        if (c0 + 512 * i < a.H) q[i] = load16_stream(a.x + t * a.ldx + c0 + 512 * i);
+    }
+    uint2 w[U];
+    uint32_t sb[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        mx_row_unit(q[i], w[i], sb[i]);
+    }
+    for (int j = 0; j < a.s.k; ++j) {
+        const int64_t r = a.s.row(t, j);
+        if (r < 0) continue;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int64_t c = c0 + 512 * i;
+            if (c >= a.H) continue;
+            *(uint2*)(codes + r * a.H + c) = w[i];
+            if ((lane & 3) == 0) a.scales[r * S + c / 32] = (uint8_t)sb[i];
+        }
+    }
+}
+
+int launch_moe_gather_mxfp8(const void* x, int64_t ldx, int64_t T, int64_t k, int64_t H, const int32_t* positions,
+                            const int32_t* source, int64_t rows, uint8_t* codes, uint8_t* scales, void* hip_stream) {
+    if (rows == 0 || H == 0) return 0;
+    GatherArgs a{(const uint16_t*)x, ldx, H, {positions, source, T, (int)k, rows}, 0, codes, scales, nullptr};
+    const int64_t waves = T * ((H + 2047) / 2048);
+    a.token_groups = (unsigned)((waves + MOE_WAVES - 1) / MOE_WAVES);
+    hipLaunchKernelGGL((moe_gather_mxfp8_kernel<4>), dim3(a.token_groups + empty_groups(rows)), dim3(MOE_THREADS), 0,
+                       (hipStream_t)hip_stream, a);
+    return (int)hipGetLastError();
+}
+
+// Row-scaled NVFP4: a workgroup takes a token, whose largest magnitude comes first.  Up to NV_UNITS vectors a thread
+// stay in registers in between; longer rows are read twice.  A lane pair holds a block of 16.
+constexpr int NV_UNITS = 4;
+
+__global__ __launch_bounds__(MOE_THREADS) void moe_gather_nvfp4_kernel(GatherArgs a) {
+    __shared__ float red[MOE_WAVES];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    uint8_t* codes = (uint8_t*)a.out;
+    const int64_t C = a.H / 2, S = a.H / 16;
+    if (blockIdx.x >= a.token_groups) {
+        const int64_t w = (int64_t)(blockIdx.x - a.token_groups) * MOE_WAVES + wave;
+        for_empty_rows(a.s.source, a.s.rows, a.s.T * a.s.k, w, (int64_t)(gridDim.x - a.token_groups) * MOE_WAVES, [&](int64_t r) {
+            for (int64_t c = 8 * lane; c < C; c += 512) *(uint2*)(codes + r * C + c) = make_uint2(0, 0);
+            for (int64_t b = lane; b < S; b += 64) a.scales[r * S + b] = 0;
+            if (lane == 0) a.s_enc[r] = 1.0f;
+        });
+        return;
+    }
+    const int64_t t = blockIdx.x;
+    const uint16_t* x = a.x + t * a.ldx;
+    const bool one = a.H <= 8 * NV_UNITS * MOE_THREADS;
+    uint4 q[NV_UNITS];
+    float m = 0.0f;
+    auto load = [&](int64_t c0) {
+#pragma unroll
+        for (int i = 0; i < NV_UNITS; ++i) {
+            const int64_t c = c0 + 8 * ((int64_t)threadIdx.x + MOE_THREADS * i);
+            q[i] = make_uint4(0, 0, 0, 0);
+            if (c < a.H) q[i] = *(const uint4*)(x + c);
+        }
+    };
+    for (int64_t c0 = 0; c0 < a.H; c0 += 8 * NV_UNITS * MOE_THREADS) {
+        load(c0);
+#pragma unroll
+        for (int i = 0; i < NV_UNITS; ++i) {
+            float v[8];
+            unpack_bf16x8(q[i], v);
+            m = __builtin_fmaxf(m, max8(v));
+        }
+    }
+    m = wave_max(m);
+    if (lane == 0) red[wave] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < MOE_WAVES; ++w) m = __builtin_fmaxf(m, red[w]);
+    const float Se = nvfp4_tensor_scale(m);
+    for (int64_t c0 = 0; c0 < a.H; c0 += 8 * NV_UNITS * MOE_THREADS) {
+        if (!one) load(c0);
+        uint32_t w[NV_UNITS], sb[NV_UNITS];
+#pragma unroll
+        for (int i = 0; i < NV_UNITS; ++i) {
+            float v[8];
+            unpack_bf16x8(q[i], v);
+            sb[i] = encode_block<8, false, false>(v, pair_max(max8(v)), Se, nullptr, 0, 0, 0, 0, &w[i]);
+        }
+        for (int j = 0; j < a.s.k; ++j) {
+            const int64_t r = a.s.row(t, j);
+            if (r < 0) continue;
+            if (c0 == 0 && threadIdx.x == 0) a.s_enc[r] = Se;
+#pragma unroll
+            for (int i = 0; i < NV_UNITS; ++i) {
+                const int64_t c = c0 + 8 * ((int64_t)threadIdx.x + MOE_THREADS * i);
+                if (c >= a.H) continue;
+                *(uint32_t*)(codes + r * C + c / 2) = w[i];
+                if ((lane & 1) == 0) a.scales[r * S + c / 16] = (uint8_t)sb[i];
+            }
+        }
+    }
+}
+
+int launch_moe_gather_nvfp4(const void* x, int64_t ldx, int64_t T, int64_t k, int64_t H, const int32_t* positions,
+                            const int32_t* source, int64_t rows, uint8_t* codes, uint8_t* scales, float* s_enc,
+                            void* hip_stream) {
+    if (rows == 0) return 0;
+    GatherArgs a{(const uint16_t*)x, ldx, H, {positions, source, T, (int)k, rows}, (unsigned)T, codes, scales, s_enc};
+    hipLaunchKernelGGL(moe_gather_nvfp4_kernel, dim3(a.token_groups + empty_groups(rows)), dim3(MOE_THREADS), 0,
+                       (hipStream_t)hip_stream, a);
+    return (int)hipGetLastError();
+}
+
+// ---------------------------------------------------------------- combine
+
+// Eight values of a row of experts' outputs.
+template <bool F32>
+struct Row8 {
+    uint4 q[F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* y, int64_t at) {
+        if constexpr (F32) {
+            q[0] = load16_stream((const float*)y + at);
+            q[1] = load16_stream((const float*)y + at + 4);
+        } else {
+            q[0] = load16_stream((const uint16_t*)y + at);
+        }
+    }
+    __device__ __forceinline__ void values(float v[8]) const {
+        if constexpr (F32) {
+            v[0] = __uint_as_float(q[0].x); v[1] = __uint_as_float(q[0].y);
+            v[2] = __uint_as_float(q[0].z); v[3] = __uint_as_float(q[0].w);
+            v[4] = __uint_as_float(q[1].x); v[5] = __uint_as_float(q[1].y);
+            v[6] = __uint_as_float(q[1].z); v[7] = __uint_as_float(q[1].w);
+        } else {
+            unpack_bf16x8(q[0], v);
+        }
+    }
+};
+
+template <bool F32>
+__device__ __forceinline__ void store8(void* y, int64_t at, const float v[8]) {
+    if constexpr (F32) {
+        *(float4*)((float*)y + at) = make_float4(v[0], v[1], v[2], v[3]);
+        *(float4*)((float*)y + at + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *(uint4*)((uint16_t*)y + at) =
+            make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
+    }
+}
+
+struct CombineArgs {
+    const void* y;
+    int64_t H;
+    MoeSlots s;
+    const float* weights;   // [T][k], or none
+    void* out;
+};
+
+// Sums in fp32 over j in ascending order, one rounding to the output's type.
+template <bool YF32, bool OF32>
+__global__ __launch_bounds__(MOE_THREADS) void moe_combine_kernel(CombineArgs a) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int64_t pieces = (a.H + 511) / 512;
+    const int64_t u = (int64_t)blockIdx.x * MOE_WAVES + wave, t = u / pieces, c = (u % pieces) * 512 + 8 * lane;
+    if (t >= a.s.T || c >= a.H) return;
+    float acc[8] = {};
+    for (int j = 0; j < a.s.k; ++j) {
+        const int64_t r = a.s.row(t, j);
+        if (r < 0) continue;
+        const float w = a.weights ? a.weights[t * a.s.k + j] : 1.0f;
+        Row8<YF32> q;
+        q.load(a.y, r * a.H + c);
+        float v[8];
+        q.values(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(w, v[e], acc[e]);
+    }
+    store8<OF32>(a.out, t * a.H + c, acc);
+}
+
+int launch_moe_combine(const void* y, int y_f32, int64_t T, int64_t k, int64_t H, const int32_t* positions, int64_t rows,
+                       const float* weights, void* out, int out_f32, void* hip_stream) {
+    if (T == 0 || H == 0) return 0;
+    hipStream_t s = (hipStream_t)hip_stream;
+    const CombineArgs a{y, H, {positions, nullptr, T, (int)k, rows}, weights, out};
+    const dim3 grid((unsigned)((T * ((H + 511) / 512) + MOE_WAVES - 1) / MOE_WAVES)), block(MOE_THREADS);
+    if (y_f32 && out_f32) hipLaunchKernelGGL((moe_combine_kernel<true, true>), grid, block, 0, s, a);
+    else if (y_f32) hipLaunchKernelGGL((moe_combine_kernel<true, false>), grid, block, 0, s, a);
+    else if (out_f32) hipLaunchKernelGGL((moe_combine_kernel<false, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((moe_combine_kernel<false, false>), grid, block, 0, s, a);
+    return (int)hipGetLastError();
+}
+
+struct CombineBwdArgs {
+    const uint16_t* dout;
+    const void* y;
+    int64_t H;
+    MoeSlots s;
+    const float* weights;
+    void* dy;
+    float* dweights;
+    unsigned token_groups;
+};
+
+// A wave takes a token: its row of dout with each of its slots' rows.
+template <bool YF32>
+__global__ __launch_bounds__(MOE_THREADS) void moe_combine_backward_kernel(CombineBwdArgs a) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    if (blockIdx.x >= a.token_groups) {
+        const int64_t w = (int64_t)(blockIdx.x - a.token_groups) * MOE_WAVES + wave;
+        for_empty_rows(a.s.source, a.s.rows, a.s.T * a.s.k, w, (int64_t)(gridDim.x - a.token_groups) * MOE_WAVES, [&](int64_t r) {
+            const float zero[8] = {};
+            for (int64_t c = 8 * lane; c < a.H; c += 512) store8<YF32>(a.dy, r * a.H + c, zero);
+        });
+        return;
+    }
+    const int64_t t = (int64_t)blockIdx.x * MOE_WAVES + wave;
+    if (t >= a.s.T) return;
+    for (int j = 0; j < a.s.k; ++j) {
+        const int64_t r = a.s.row(t, j);
+        float dot = 0.0f;
+        if (r >= 0) {
+            const float w = a.weights[t * a.s.k + j];
+            for (int64_t c = 8 * lane; c < a.H; c += 512) {
+                float d[8], v[8], o[8];
+                unpack_bf16x8(*(const uint4*)(a.dout + t * a.H + c), d);
+                Row8<YF32> q;
+                q.load(a.y, r * a.H + c);
+                q.values(v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    dot = __builtin_fmaf(d[e], v[e], dot);
+                    o[e] = w * d[e];
+                }
+                store8<YF32>(a.dy, r * a.H + c, o);
+            }
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
+        if (lane == 0) a.dweights[t * a.s.k + j] = dot;
+    }
+}
+
+int launch_moe_combine_backward(const void* dout, const void* y, int y_f32, int64_t T, int64_t k, int64_t H,
+                                const int32_t* positions, const int32_t* source, int64_t rows, const float* weights,
+                                void* dy, float* dweights, void* hip_stream) {
+    if (T * k == 0 && rows == 0) return 0;
+    hipStream_t s = (hipStream_t)hip_stream;
+    const unsigned tg = (unsigned)((T + MOE_WAVES - 1) / MOE_WAVES);
+    const CombineBwdArgs a{(const uint16_t*)dout, y, H, {positions, source, T, (int)k, rows}, weights, dy, dweights, tg};
+    const dim3 grid(tg + empty_groups(rows)), block(MOE_THREADS);
+    if (y_f32) hipLaunchKernelGGL((moe_combine_backward_kernel<true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((moe_combine_backward_kernel<false>), grid, block, 0, s, a);
+    return (int)hipGetLastError();
+}
+
+}  // namespace bsq

@@ -7,7 +7,8 @@
  * NVFP4 dequantization, the MXFP8 cast, the standalone Hadamard transform, and the
  * block-scaled GEMM C = A * B^T that consumes the quantized operands with fp32
  * accumulation; around them the products of a gated feed-forward block with their backward
- * pass, products of a few bf16 tokens with NVFP4 weights, and gradient clipping.
+ * pass, products of a few bf16 tokens with NVFP4 weights, and gradient clipping; and for tokens
+ * that have weights of their own the way to their experts and back, and low-rank adapters.
  *
  * Conventions shared by every entry point:
  *   - Tensors are row-major and contiguous.  A bf16 tensor x has shape [rows][cols].
@@ -525,6 +526,100 @@ int grad_clip(const void* const* grads, void* const* outs, const int64_t* numels
 
 int clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes,
                    int64_t count, double max_norm, float* norm, void* workspace, void* hip_stream);
+
+/*
+ * Tokens and their experts.  A token has k slots; slot i = t k + j is the j-th expert's of token t.  moe_sort orders the
+ * slots by expert for blockscaled_grouped_gemm, whose `offsets` it writes; the gathers copy tokens to their
+ * experts' rows, as bf16 or as the quantized operand; moe_combine adds the experts' rows up for each token.
+ * Arrays of ids, positions, sources, weights and per-row scales are aligned to their elements, everything else
+ * to 16 bytes.  Nothing is copied to the host.  No output overlaps another argument.
+ *
+ * moe_sort -- a stable sort of slots by expert, each expert's rows starting at a multiple of align.
+ *   experts    int32 (id_bytes 4) or int64 (8) [slots], device: a slot's expert.  A slot whose id is outside
+ *              [0, num_experts) is dropped (an expert that is full, or on another rank).
+ *   slots in [0, 2^30], num_experts in [1, 1024], align a power of two up to 256 (BSQ_GROUP_K needs 32).
+ *   rows       rows of the sorted order; at least moe_sort_rows(slots, num_experts, align), which holds any choice of
+ *              experts: (slots + min(slots, num_experts) (align - 1)) rounded down to a multiple of align.
+ *   offsets    int64[num_experts + 1] (device): the groups' starts; offsets[num_experts] is the end of the last
+ *              one, its padding included.
+ *   positions  int32[slots] (device): each slot's row, -1 for a dropped one.
+ *   source     int32[rows] (device): each row's slot, -1 for a row without one (padding, and what lies behind
+ *              the last group).
+ *   workspace  device scratch of moe_sort_workspace_bytes(slots, num_experts) bytes, as for nvfp4_quantize.
+ * The size queries return -1 for sizes out of range.
+ */
+int64_t moe_sort_rows(int64_t slots, int64_t num_experts, int64_t align);
+int64_t moe_sort_workspace_bytes(int64_t slots, int64_t num_experts);
+int moe_sort(const void* experts, int id_bytes, int64_t slots, int64_t num_experts, int64_t align, int64_t rows,
+             int64_t* offsets, int32_t* positions, int32_t* source, void* workspace, void* hip_stream);
+
+/*
+ * moe_gather -- out[r] = x[source[r] / k], zeros where a row has no source: tokens in the order of their experts.
+ * Every row of out is written.  Its gradient is moe_combine without weights.
+ *   x          bf16, token t at x + t * ldx elements; ldx >= width, ldx % 8 == 0.  width % 8 == 0.
+ *   positions  int32[tokens][k], source int32[rows] as moe_sort writes them.  Both are read; entries outside their range
+ *              count as none, and what is written to a row on which the two disagree is unspecified.
+ *   tokens <= 2^23, k <= 64, tokens * ceil(width / 512) <= 2^25.
+ * moe_gather_nvfp4_rowscaled -- nvfp4_quantize_rowscaled (BSQ_RNE, no transform) of that out, bit for bit, without the
+ * copy in between: a token is quantized once and its codes written to its k rows.  width % 16 == 0.
+ *   codes [rows][width/2], scales [rows][width/16], s_enc_rows float[rows] (device).
+ * moe_gather_mxfp8 -- likewise mxfp8_quantize with BSQ_ROW.  width % 32 == 0.  A value that is not finite becomes the NaN
+ * code, under the scale byte 247 (the cast's codes of such a block depend on its neighbours).
+ *   row_codes [rows][width], row_scales [rows][width/32] (device).
+ */
+int moe_gather(int64_t tokens, int64_t k, int64_t width, const void* x, int64_t ldx, const int32_t* positions,
+               const int32_t* source, int64_t rows, void* out, void* hip_stream);
+int moe_gather_nvfp4_rowscaled(int64_t tokens, int64_t k, int64_t width, const void* x, int64_t ldx,
+                               const int32_t* positions, const int32_t* source, int64_t rows, uint8_t* codes,
+                               uint8_t* scales, float* s_enc_rows, void* hip_stream);
+int moe_gather_mxfp8(int64_t tokens, int64_t k, int64_t width, const void* x, int64_t ldx, const int32_t* positions,
+                     const int32_t* source, int64_t rows, uint8_t* row_codes, uint8_t* row_scales, void* hip_stream);
+
+/*
+ * moe_combine -- out[t] = sum over j of weights[t][j] * y[positions[t][j]], in fp32 in the order of j, rounded once.
+ *   y          [rows][width], y_dtype BSQ_OUT_BF16 or BSQ_OUT_F32; width % 8 == 0.
+ *   weights    float[tokens][k] (device), or NULL: every weight is 1.
+ *   out        [tokens][width], out_dtype BSQ_OUT_BF16 or BSQ_OUT_F32.
+ * A dropped slot (positions outside [0, rows)) adds nothing whatever its weight; a token without slots gets zeros.
+ *
+ * moe_combine_backward -- its gradients: dy[positions[t][j]] = weights[t][j] * dout[t], zeros in rows without a source,
+ * and dweights[t][j] = <dout[t], y[positions[t][j]]> in fp32, 0 for a dropped slot.
+ *   dout [tokens][width] bf16; dy [rows][width] of y's type; dweights float[tokens][k].
+ * Sizes as for moe_gather.
+ */
+int moe_combine(int64_t tokens, int64_t k, int64_t width, const void* y, int y_dtype, int64_t rows,
+                const int32_t* positions, const float* weights, void* out, int out_dtype, void* hip_stream);
+int moe_combine_backward(int64_t tokens, int64_t k, int64_t width, const void* dout, const void* y, int y_dtype,
+                         int64_t rows, const int32_t* positions, const int32_t* source, const float* weights, void* dy,
+                         float* dweights, void* hip_stream);
+
+/*
+ * Low-rank adapters of many requests, each token with its own: out[m] = y[m] + s_a (x[m] A_a^T) B_a^T, a = adapters[m].
+ *   x          bf16, token m at x + m * ldx elements; ldx >= K, ldx % 8 == 0.
+ *   adapters   int32[M] (device); outside [0, num_adapters): the token has none and gets y as it is.
+ *   lora_a     [num_adapters][rank][K], lora_b [num_adapters][N][rank] bf16; rank a multiple of 8 up to 256
+ *              (smaller ones are padded with zeros).  scales float[num_adapters] (device), or NULL: 1.
+ *   workspace  device scratch of lora_workspace_bytes(M, rank) bytes, as for nvfp4_quantize.
+ * Products of bf16 values are exact and added up in fp32; the result is rounded once, to y's type.  A NaN or an infinity
+ * in a token reaches that token's outputs only, one in an adapter the tokens that have it.  Tokens of one adapter should
+ * stand together where there are many: an adapter is read once for every 16 tokens among which it occurs.
+ *
+ * lora_add -- beside any projection, whose output y is given.
+ *   y, out     bf16 or fp32 (y_dtype), rows ldy and ldo elements apart (a projection's slice of a wider output); out
+ *              is y itself with ldo == ldy (in place), or overlaps no other argument.  Aligned to their elements.
+ *   K % 8 == 0, K < 2^24; M <= 2^20; N any with ceil(M / 16) ceil(N / 256) < 2^24.
+ *
+ * nvfp4_lora_matvec -- beside NVFP4 weights that all tokens share: nvfp4_matvec's arguments and sizes, and its product
+ * with the adapters' added in fp32 before the one rounding of y.
+ */
+int64_t lora_workspace_bytes(int64_t tokens, int64_t rank);
+int lora_add(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t num_adapters, const void* x, int64_t ldx,
+             const int32_t* adapters, const void* lora_a, const void* lora_b, const float* scales, const void* y,
+             int64_t ldy, void* out, int64_t ldo, int y_dtype, void* workspace, void* hip_stream);
+int nvfp4_lora_matvec(int flags, int64_t M, int64_t N, int64_t K, const void* x, int64_t ldx, const uint8_t* w_codes,
+                      const uint8_t* w_scales, const float* w_s_enc, int64_t rank, int64_t num_adapters,
+                      const int32_t* adapters, const void* lora_a, const void* lora_b, const float* scales, void* y,
+                      int y_dtype, void* workspace, void* hip_stream);
 
 /* Message of the last failing call on this thread ("" if none).  Host memory owned
  * by the library; valid until the thread's next call. */
