@@ -682,7 +682,7 @@ int64_t sorted_rows(int64_t n, int64_t E, int64_t align) {
 }
 
 int sort_sizes_check(const char* fn, int64_t slots, int64_t experts, int64_t align) {
-    if (slots < 0 || slots > (int64_t)1 << 30) return fail(BSQ_ERR_SHAPE, "%s: %lld slots are not in [0, 2^30]", fn, (long long)slots);
+    if (slots < 0 || slots > (int64_t)1 << 25) return fail(BSQ_ERR_SHAPE, "%s: %lld slots are not in [0, 2^25]", fn, (long long)slots);
     if (experts < 1 || experts > 1024) return fail(BSQ_ERR_SHAPE, "%s: %lld experts are not in [1, 1024]", fn, (long long)experts);
     if (align < 1 || align > 256 || (align & (align - 1)) != 0)
         return fail(BSQ_ERR_ARG, "%s: align (%lld) must be a power of two up to 256", fn, (long long)align);
@@ -696,6 +696,7 @@ int slots_check(const char* fn, int64_t T, int64_t k, int64_t H, int64_t step, i
     if (T > (int64_t)1 << 23 || H > (int64_t)1 << 24 || T * ((H + 511) / 512) > (int64_t)1 << 25)
         return fail(BSQ_ERR_SHAPE, "%s: %lld tokens of width %lld are too many for one launch", fn, (long long)T, (long long)H);
     if (k > 64) return fail(BSQ_ERR_SHAPE, "%s: k (%lld) must be at most 64", fn, (long long)k);
+    if (T * k > (int64_t)1 << 25) return fail(BSQ_ERR_SHAPE, "%s: %lld slots exceed 2^25", fn, (long long)(T * k));
     if (rows > 0x7FFFFFFF) return fail(BSQ_ERR_SHAPE, "%s: %lld rows exceed 2^31 - 1", fn, (long long)rows);
     if (T * k > 0 && !positions) return fail(BSQ_ERR_NULL, "%s: positions is NULL", fn);
     if (unaligned(positions, 4)) return fail(BSQ_ERR_ALIGN, "%s: positions is not aligned", fn);
@@ -833,7 +834,7 @@ extern "C" {
 
 int64_t lora_workspace_bytes(int64_t tokens, int64_t rank) {
     if (tokens < 0 || tokens > (int64_t)1 << 20 || rank < 8 || rank > 256 || rank % 8 != 0) return -1;
-    return tokens * rank * 4;
+    return (tokens + 15) / 16 * 16 * ((rank + 31) / 32 * 32) * 6;   // three bf16 parts of every down product, or fp32
 }
 
 int lora_add(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t num_adapters, const void* x, int64_t ldx,

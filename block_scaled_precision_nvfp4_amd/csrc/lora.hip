@@ -13,7 +13,6 @@ namespace bsq {
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 
 constexpr int LORA_TOKENS = 16;
-constexpr int LORA_DOWN_WAVES = 16;    // share K
 
 // The ids of a tile's adapters: lane i holds token i % 16's, -1 for none.
 __device__ __forceinline__ int lora_ids(const LoraArgs& a, int64_t m0) {
@@ -33,131 +32,263 @@ __device__ __forceinline__ void for_adapters(int ids, int first, int step, F&& b
     }
 }
 
-// t[m][rank] of a tile: blockIdx.x tile, .y which of its adapters, .z 16 NR ranks.  The waves share K, 64
-// elements of every row at a time (whole 128-byte lines), and are joined in LDS.
-template <int NR>
-__global__ __launch_bounds__(64 * LORA_DOWN_WAVES) void lora_down_kernel(LoraArgs a) {
-    __shared__ float red[LORA_DOWN_WAVES][NR][LORA_TOKENS][16 + 1];
+// t of a tile: blockIdx.x tile, .y which of its adapters, .z 16 NR ranks.  The waves share K, 64 elements (a
+// 128-byte line) of every row at a time.  A wave reads whole lines, 8 lanes each, and turns them to the matrix
+// instruction's order through LDS of its own: read in that order, neighbouring lanes would touch 16 lines, 16 bytes
+// of each, at a quarter of the rate.  D pieces are in flight in registers.  The waves' sums are joined in LDS.
+constexpr int LORA_PITCH = 144;   // bytes between rows in LDS: the fragments' reads cover all banks
+constexpr int lora_waves(int nr) { return nr == 4 ? 8 : 16; }
+
+template <int NR, bool PARTS>
+__global__ __launch_bounds__(64 * lora_waves(NR)) void lora_down_kernel(LoraArgs a) {
+    constexpr int W = lora_waves(NR), D = NR == 1 ? 4 : 2, ROWS = LORA_TOKENS * (NR + 1);
+    static_assert(W * NR * LORA_TOKENS * 17 * 4 <= W * ROWS * LORA_PITCH, "the join takes the rows' place");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[W * ROWS * LORA_PITCH];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int waves = (int)(blockDim.x >> 6), r16 = lane & 15, g = lane >> 4;
-    const int64_t m0 = (int64_t)blockIdx.x * LORA_TOKENS, rank0 = (int64_t)blockIdx.z * 16 * NR;
+    const int r16 = lane & 15, g = lane >> 4, row8 = lane >> 3, k8 = 8 * (lane & 7);
+    // neighbouring tiles, which mostly share an adapter, to one XCD (workgroups go to the 8 XCDs in turn)
+    const unsigned per = gridDim.x / 8, tile = blockIdx.x < per * 8 ? blockIdx.x % 8 * per + blockIdx.x / 8 : blockIdx.x;
+    const int64_t m0 = (int64_t)tile * LORA_TOKENS;
+    const int rank0 = blockIdx.z * 16 * NR, K = (int)a.K, pieces = (K + 63) / 64;
     const int ids = lora_ids(a, m0);
-    const int64_t mx = m0 + r16 < a.M ? m0 + r16 : a.M - 1;   // rows past the end repeat the last one
-    const uint16_t* x = a.x + mx * a.ldx;
+    uint8_t* mine = lds + wave * ROWS * LORA_PITCH;
     for_adapters(ids, blockIdx.y, gridDim.y, [&](int id) {
-        floatx4 acc[NR];
-        const uint16_t* w[NR];
+        const uint32_t rows = (uint32_t)__ballot(ids == id) & 0xFFFFu;   // the tile's tokens with this adapter
+        // a lane's rows: tokens row8 and 8 + row8, ranks rank0 + 8 i + row8; the others count as zeros
+        const uint16_t* x = a.x + (m0 + row8) * a.ldx + k8;
+        const uint16_t* w = a.a + ((int64_t)id * a.r + rank0 + row8) * a.K + k8;
+        uint4 v[D][2 * (NR + 1)];
+        auto load = [&](int d, int c) {
+            const bool in = 64 * c + k8 < K;
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            acc[n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-            const int64_t rank = rank0 + 16 * n + r16;
-            w[n] = a.a + ((int64_t)id * a.r + (rank < a.r ? rank : a.r - 1)) * a.K;
-        }
-        for (int64_t k0 = (int64_t)wave * 64; k0 < a.K; k0 += 64 * waves) {
+            for (int i = 0; i < 2 * (NR + 1); ++i) {
+                v[d][i] = make_uint4(0, 0, 0, 0);
+                const bool on = i < 2 ? (rows >> (8 * i + row8)) & 1 : rank0 + 8 * (i - 2) + row8 < a.r;
+                if (on && in) v[d][i] = *(const uint4*)((i < 2 ? x + 8 * i * a.ldx : w + 8 * (i - 2) * a.K) + 64 * c);
+            }
+        };
+        floatx4 acc[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) acc[n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+        auto use = [&](int d) {
+#pragma unroll
+            for (int i = 0; i < 2 * (NR + 1); ++i) *(uint4*)(mine + (8 * i + row8) * LORA_PITCH + 2 * k8) = v[d][i];
+            __builtin_amdgcn_wave_barrier();   // a wave's LDS accesses run in order
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int64_t k = k0 + 16 * g + 8 * h;
-                bf16x8_t xv = {}, wv[NR] = {};
-                if (k < a.K) {
-                    xv = *(const bf16x8_t*)(x + k);
+                const uint8_t* f = mine + r16 * LORA_PITCH + 32 * g + 16 * h;
+                const bf16x8_t xv = *(const bf16x8_t*)f;
 #pragma unroll
-                    for (int n = 0; n < NR; ++n) wv[n] = *(const bf16x8_t*)(w[n] + k);
-                }
-#pragma unroll
-                for (int n = 0; n < NR; ++n) acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, wv[n], acc[n], 0, 0, 0);
+                for (int n = 0; n < NR; ++n)
+                    acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, *(const bf16x8_t*)(f + 16 * (n + 1) * LORA_PITCH),
+                                                                     acc[n], 0, 0, 0);
             }
-        }
-        __syncthreads();   // the adapter before this one has been added up
+            __builtin_amdgcn_wave_barrier();
+        };
+        const int count = pieces > wave ? (pieces - wave - 1) / W + 1 : 0;   // pieces wave, wave + W, ...
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            if (d < count) load(d, wave + d * W);
+        for (int n = 0; n < count; n += D)
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+                if (n + d < count) {
+                    use(d);
+                    if (n + d + D < count) load(d, wave + (n + d + D) * W);
+                }
+        __syncthreads();
+        float* red = (float*)lds;   // [wave][NR][16][17]
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) red[wave][n][4 * g + i][r16] = acc[n][i];
+            for (int i = 0; i < 4; ++i) red[((wave * NR + n) * LORA_TOKENS + 4 * g + i) * 17 + r16] = acc[n][i];
         __syncthreads();
-        for (int i = threadIdx.x; i < LORA_TOKENS * 16 * NR; i += blockDim.x) {
-            const int m = i / (16 * NR), n = i / 16 % NR, q = i % 16;
-            const int64_t rank = rank0 + 16 * n + q;
-            if (rank >= a.r || m0 + m >= a.M) continue;
-            const int mine = a.adapters[m0 + m];
-            if (mine != id) continue;
-            float s = 0.0f;
-            for (int v = 0; v < waves; ++v) s += red[v][n][m][q];
-            a.t[(m0 + m) * a.r + rank] = s;
+        for (int i = threadIdx.x; i < LORA_TOKENS * 16 * NR; i += 64 * W) {
+            const int m = i / (16 * NR), n = i / 16 % NR, q = i % 16, rank = rank0 + 16 * n + q;
+            if (!((rows >> m) & 1)) continue;
+            float t = 0.0f;
+#pragma unroll
+            for (int u = 0; u < W; ++u) t += red[((u * NR + n) * LORA_TOKENS + m) * 17 + q];
+            if constexpr (PARTS) {
+                if (rank >= a.r) continue;
+                uint16_t p[3];
+                lora_split(t, p);
+                uint16_t* at = (uint16_t*)a.t + ((int64_t)tile * lora_steps(a.r) + rank / 32) * 3 * 512 + (m + 16 * (rank / 8 % 4)) * 8 + rank % 8;
+                at[0] = p[0];
+                at[512] = p[1];
+                at[1024] = p[2];
+            } else if (rank < a.r) {
+                a.t[(m0 + m) * a.r + rank] = t;
+            }
         }
+        __syncthreads();   // before the next adapter's rows
     });
 }
 
-// The up products of a tile by 64 columns per wave.  B's rows take the matrix instruction's rows, so that a lane
-// ends with 16 adjacent columns of one token: row 4 g + i of block b stands for column 16 g + 4 b + i.  t goes in as
-// three bf16 parts that add up to it exactly.
+// The up products of 64 columns by a tile of 16 tokens per wave.  The workgroup's waves take neighbouring tiles, which
+// mostly share an adapter: its 64 rows of B come through LDS, whole lines at a time, for all of them.  t comes as the
+// matrix instruction's fragments, in three bf16 parts that add up to it exactly.  Column r16 of block b stands for
+// column 4 r16 + b, so that a lane ends with 4 adjacent columns of each of 4 tokens (4 g + i) and 16 lanes read and
+// write 128 (or 256) adjacent bytes of y.
 constexpr int LORA_UP_WAVES = 4, LORA_COLS = 64;
 
-template <bool F32>
+// RS: steps of 32 ranks
+template <bool F32, int RS>
 __global__ __launch_bounds__(64 * LORA_UP_WAVES) void lora_up_kernel(LoraArgs a) {
+    constexpr int PITCH = 64 * RS + 16;   // bytes between rows in LDS; the fragments' reads cover all banks
+    __shared__ __attribute__((aligned(16))) uint8_t lds[LORA_COLS * PITCH];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int r16 = lane & 15, g = lane >> 4;
-    const int64_t cols = (a.N + LORA_COLS * LORA_UP_WAVES - 1) / (LORA_COLS * LORA_UP_WAVES);
-    const int64_t m0 = blockIdx.x / cols * LORA_TOKENS, n0 = (blockIdx.x % cols * LORA_UP_WAVES + wave) * LORA_COLS;
-    if (n0 >= a.N) return;
-    const int ids = lora_ids(a, m0);   // lane's token r16
-    const int64_t m = m0 + r16;
-    const float* t = a.t + (m < a.M ? m : a.M - 1) * a.r;
-    const int64_t c0 = n0 + 16 * g;
-    float add[16] = {};
-    float scale = 0.0f;
-    for_adapters(ids, 0, 1, [&](int id) {
-        floatx4 acc[4];
+    const int64_t cols = (a.N + LORA_COLS - 1) / LORA_COLS, n0 = blockIdx.x % cols * LORA_COLS;
+    const int64_t tile0 = blockIdx.x / cols * LORA_UP_WAVES, m0 = (tile0 + wave) * LORA_TOKENS;
+    typedef typename std::conditional<F32, float, uint16_t>::type item;
+    typedef typename std::conditional<F32, uint4, uint2>::type vec;
+    const bool whole = n0 + LORA_COLS <= a.N && a.vec;   // else element by element
+    const int64_t c0 = n0 + 4 * r16;
+    const int steps = lora_steps(a.r), cpr = a.r / 8;    // 16-byte pieces of a row of B
+    const int64_t ml = tile0 * LORA_TOKENS + lane;       // lane's of the workgroup's 64 tokens
+    int all = ml < a.M ? a.adapters[ml] : -1;
+    all = all >= 0 && all < a.L ? all : -1;
+    bf16x8_t part[RS][3];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) acc[b] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int q0 = 0; q0 < a.r; q0 += 32) {
-            const int q = q0 + 8 * g;
-            bf16x8_t part[3] = {};
-            if (q < a.r && ids == id) lora_split8(t + q, part);
+    for (int q = 0; q < RS; ++q)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int64_t n = n0 + 16 * (r16 >> 2) + 4 * b + (r16 & 3);
-                bf16x8_t w = {};
-                if (q < a.r && n < a.N) w = *(const bf16x8_t*)(a.b + ((int64_t)id * a.N + n) * a.r + q);
+        for (int p = 0; p < 3; ++p) {
+            part[q][p] = bf16x8_t{};   // past r nothing is written
+            if (32 * q + 8 * g < a.r && m0 < a.M)
+                part[q][p] = *(const bf16x8_t*)((const uint16_t*)a.t + (((tile0 + wave) * steps + q) * 3 + p) * 512 + 8 * lane);
+        }
+    vec v[4];
 #pragma unroll
-                for (int p = 2; p >= 0; --p) acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, part[p], acc[b], 0, 0, 0);
+    for (int i = 0; i < 4; ++i)
+        if (whole && m0 + 4 * g + i < a.M) v[i] = *(const vec*)((const item*)a.y + (m0 + 4 * g + i) * a.ldy + c0);
+    int mine[4];   // the adapters of the lane's tokens of y
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mine[i] = __shfl(all, 16 * wave + 4 * g + i);
+    floatx4 add[4];
+    float scale[4];
+    for (uint64_t left = __ballot(all >= 0); left != 0;) {   // the same in every wave
+        const int id = __builtin_amdgcn_readlane(all, __builtin_ctzll(left));
+        const uint64_t here = __ballot(all == id);
+        left &= ~here;
+        for (int e = threadIdx.x; e < LORA_COLS * cpr; e += 64 * LORA_UP_WAVES) {
+            const int row = e / cpr, piece = e - row * cpr;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (n0 + row < a.N) w = *(const uint4*)(a.b + ((int64_t)id * a.N + n0 + row) * a.r + 8 * piece);
+            *(uint4*)(lds + ((row & 3) * 16 + (row >> 2)) * PITCH + 16 * piece) = w;   // block b's rows side by side
+        }
+        const float sc = a.scales ? a.scales[id] : 1.0f;
+        __syncthreads();
+        if ((here >> (16 * wave)) & 0xFFFFu) {
+            floatx4 acc[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) acc[b] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int q = 0; q < RS; ++q)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    bf16x8_t w = {};
+                    if (32 * q + 8 * g < a.r) w = *(const bf16x8_t*)(lds + (16 * b + r16) * PITCH + 64 * q + 16 * g);
+#pragma unroll
+                    for (int p = 2; p >= 0; --p) acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part[q][p], w, acc[b], 0, 0, 0);
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (mine[i] == id) {
+                    add[i] = floatx4{acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
+                    scale[i] = sc;
+                }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t m = m0 + 4 * g + i;
+        const bool has = mine[i] >= 0;
+        if (m >= a.M || (!has && a.out == a.y)) continue;
+        item* out = (item*)a.out + m * a.ldo + c0;
+        if (whole) {
+            if (has) {
+                if constexpr (F32) {
+                    v[i] = make_uint4(__float_as_uint(__builtin_fmaf(scale[i], add[i][0], __uint_as_float(v[i].x))),
+                                      __float_as_uint(__builtin_fmaf(scale[i], add[i][1], __uint_as_float(v[i].y))),
+                                      __float_as_uint(__builtin_fmaf(scale[i], add[i][2], __uint_as_float(v[i].z))),
+                                      __float_as_uint(__builtin_fmaf(scale[i], add[i][3], __uint_as_float(v[i].w))));
+                } else {
+                    v[i] = make_uint2(bf16x2_rne(__builtin_fmaf(scale[i], add[i][0], bf16_lo(v[i].x)),
+                                                 __builtin_fmaf(scale[i], add[i][1], bf16_hi(v[i].x))),
+                                      bf16x2_rne(__builtin_fmaf(scale[i], add[i][2], bf16_lo(v[i].y)),
+                                                 __builtin_fmaf(scale[i], add[i][3], bf16_hi(v[i].y))));
+                }
             }
+            *(vec*)out = v[i];
+            continue;
         }
-        if (ids == id) {
-            scale = a.scales ? a.scales[id] : 1.0f;
+        const item* y = (const item*)a.y + m * a.ldy + c0;
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) add[4 * b + i] = acc[b][i];
-        }
-    });
-    if (m >= a.M || (ids < 0 && a.out == a.y)) return;
-    for (int i = 0; i < 16; ++i) {
-        const int64_t n = c0 + i;
-        if (n >= a.N) break;
-        if constexpr (F32) {
-            const float y = ((const float*)a.y)[m * a.ldy + n];
-            ((float*)a.out)[m * a.ldo + n] = ids < 0 ? y : __builtin_fmaf(scale, add[i], y);
-        } else {
-            const uint16_t y = ((const uint16_t*)a.y)[m * a.ldy + n];
-            ((uint16_t*)a.out)[m * a.ldo + n] =
-                ids < 0 ? y : (uint16_t)bf16x2_rne(__builtin_fmaf(scale, add[i], __uint_as_float((uint32_t)y << 16)), 0.0f);
+        for (int b = 0; b < 4; ++b) {
+            if (c0 + b >= a.N) continue;
+            item o = y[b];
+            if (has) {
+                if constexpr (F32) o = __builtin_fmaf(scale[i], add[i][b], o);
+                else o = (uint16_t)bf16x2_rne(__builtin_fmaf(scale[i], add[i][b], __uint_as_float((uint32_t)o << 16)), 0.0f);
+            }
+            out[b] = o;
         }
     }
 }
 
-int launch_lora_down(const LoraArgs& a, hipStream_t s) {
-    if (a.M == 0 || a.r == 0) return 0;
+// Few tokens: a thread takes one value of y, so that any mixture of adapters goes at once.
+constexpr int LORA_FEW = 64;
+
+template <bool F32>
+__global__ __launch_bounds__(256) void lora_up_few_kernel(LoraArgs a) {
+    const int64_t m = blockIdx.y, n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (n >= a.N) return;
+    if constexpr (F32) {
+        ((float*)a.out)[m * a.ldo + n] = lora_added(a, m, n, ((const float*)a.y)[m * a.ldy + n]);
+    } else {
+        const uint16_t y = ((const uint16_t*)a.y)[m * a.ldy + n];
+        const int id = a.adapters[m];
+        ((uint16_t*)a.out)[m * a.ldo + n] =
+            id < 0 || id >= a.L ? y : (uint16_t)bf16x2_rne(lora_added(a, m, n, __uint_as_float((uint32_t)y << 16)), 0.0f);
+    }
+}
+
+template <bool PARTS>
+static int launch_down(const LoraArgs& a, hipStream_t s) {
     const int64_t tiles = (a.M + LORA_TOKENS - 1) / LORA_TOKENS;
+    // a workgroup for each adapter that a tile can have while the tiles are few
     const unsigned many = tiles <= 16 ? (unsigned)(a.M < LORA_TOKENS ? a.M : LORA_TOKENS) : 1u;
     if (a.r <= 16)
-        hipLaunchKernelGGL(lora_down_kernel<1>, dim3((unsigned)tiles, many, 1), dim3(64 * LORA_DOWN_WAVES), 0, s, a);
+        hipLaunchKernelGGL((lora_down_kernel<1, PARTS>), dim3((unsigned)tiles, many, 1), dim3(64 * lora_waves(1)), 0, s, a);
+    else if (a.r <= 32)
+        hipLaunchKernelGGL((lora_down_kernel<2, PARTS>), dim3((unsigned)tiles, many, 1), dim3(64 * lora_waves(2)), 0, s, a);
     else
-        hipLaunchKernelGGL(lora_down_kernel<4>, dim3((unsigned)tiles, many, (unsigned)((a.r + 63) / 64)),
-                           dim3(64 * LORA_DOWN_WAVES), 0, s, a);
+        hipLaunchKernelGGL((lora_down_kernel<4, PARTS>), dim3((unsigned)tiles, many, (unsigned)((a.r + 63) / 64)),
+                           dim3(64 * lora_waves(4)), 0, s, a);
     return (int)hipGetLastError();
 }
 
+int launch_lora_down(const LoraArgs& a, hipStream_t s) { return launch_down<false>(a, s); }
+
 int64_t lora_up_groups(int64_t M, int64_t N) {
-    return ((M + LORA_TOKENS - 1) / LORA_TOKENS) * ((N + LORA_COLS * LORA_UP_WAVES - 1) / (LORA_COLS * LORA_UP_WAVES));
+    const int64_t tokens = LORA_TOKENS * LORA_UP_WAVES;
+    return ((M + tokens - 1) / tokens) * ((N + LORA_COLS - 1) / LORA_COLS);
+}
+
+template <bool F32>
+static int launch_up(const LoraArgs& a, hipStream_t s) {
+    if (a.M <= LORA_FEW) {
+        hipLaunchKernelGGL((lora_up_few_kernel<F32>), dim3((unsigned)((a.N + 255) / 256), (unsigned)a.M), dim3(256), 0, s, a);
+        return (int)hipGetLastError();
+    }
+    const dim3 grid((unsigned)lora_up_groups(a.M, a.N)), block(64 * LORA_UP_WAVES);
+    if (a.r <= 32) hipLaunchKernelGGL((lora_up_kernel<F32, 1>), grid, block, 0, s, a);
+    else if (a.r <= 64) hipLaunchKernelGGL((lora_up_kernel<F32, 2>), grid, block, 0, s, a);
+    else if (a.r <= 128) hipLaunchKernelGGL((lora_up_kernel<F32, 4>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((lora_up_kernel<F32, 8>), grid, block, 0, s, a);
+    return (int)hipGetLastError();
 }
 
 int launch_lora_add(int f32, int64_t M, int64_t N, int64_t K, int64_t r, int64_t L, const void* x, int64_t ldx,
@@ -166,13 +297,12 @@ int launch_lora_add(int f32, int64_t M, int64_t N, int64_t K, int64_t r, int64_t
     if (M == 0 || N == 0) return 0;
     hipStream_t s = (hipStream_t)hip_stream;
     const LoraArgs a{M, N, K, (int)r, L, (const uint16_t*)x, ldx, adapters, (const uint16_t*)lora_a, (const uint16_t*)lora_b,
-                     scales, workspace, y, ldy, out, ldo};
-    const int e = launch_lora_down(a, s);
+                     scales, workspace, y, ldy, out, ldo,
+                     (((uintptr_t)y | (uintptr_t)out | (uintptr_t)(ldy * (f32 ? 4 : 2)) | (uintptr_t)(ldo * (f32 ? 4 : 2))) &
+                      (f32 ? 15 : 7)) == 0};
+    const int e = M <= LORA_FEW ? launch_down<false>(a, s) : launch_down<true>(a, s);
     if (e) return e;
-    const dim3 grid((unsigned)lora_up_groups(M, N)), block(64 * LORA_UP_WAVES);
-    if (f32) hipLaunchKernelGGL(lora_up_kernel<true>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(lora_up_kernel<false>, grid, block, 0, s, a);
-    return (int)hipGetLastError();
+    return f32 ? launch_up<true>(a, s) : launch_up<false>(a, s);
 }
 
 }  // namespace bsq

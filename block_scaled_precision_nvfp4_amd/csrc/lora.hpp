@@ -17,31 +17,30 @@ struct LoraArgs {
     const uint16_t* a;          // [L][r][K]
     const uint16_t* b;          // [L][N][r]
     const float* scales;        // [L], or none
-    float* t;                   // [M][r]: the down products
+    float* t;                   // the down products: [M][r], or fragments of three bf16 parts (lora.hip)
     const void* y;
     int64_t ldy;
     void* out;
     int64_t ldo;
+    bool vec;                   // 4 columns of y and out are one aligned access, from every 4th on
 };
 
 int launch_lora_down(const LoraArgs& a, hipStream_t s);
 
-// Eight values as three bf16 parts that add up to each exactly (8 bits of the significand each, cut, not
-// rounded, so that a large value does not become infinite).  An infinity or NaN goes into the first part alone.
-__device__ __forceinline__ void lora_split8(const float* t, bf16x8_t (&part)[3]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float v = t[i];
-        const uint32_t u = __float_as_uint(v);
-        const bool fin = (u & 0x7F800000u) != 0x7F800000u;
-        const uint32_t hi = (u & 0xFFFF0000u) | (!fin && (u & 0x7FFFFFu) ? 0x400000u : 0u);
-        const float r1 = v - __uint_as_float(hi);
-        const uint32_t mid = __float_as_uint(r1) & 0xFFFF0000u;
-        const float r2 = r1 - __uint_as_float(mid);
-        part[0][i] = __builtin_bit_cast(__bf16, (uint16_t)(hi >> 16));
-        part[1][i] = __builtin_bit_cast(__bf16, (uint16_t)(fin ? mid >> 16 : 0u));
-        part[2][i] = __builtin_bit_cast(__bf16, (uint16_t)(fin ? __float_as_uint(r2) >> 16 : 0u));
-    }
+__host__ __device__ constexpr int lora_steps(int r) { return (r + 31) / 32; }
+
+// A value as three bf16 parts that add up to it exactly (8 bits of the significand each, cut, not rounded, so that a
+// large value does not become infinite).  An infinity or NaN goes into the first part alone.
+__device__ __forceinline__ void lora_split(float v, uint16_t (&part)[3]) {
+    const uint32_t u = __float_as_uint(v);
+    const bool fin = (u & 0x7F800000u) != 0x7F800000u;
+    const uint32_t hi = (u & 0xFFFF0000u) | (!fin && (u & 0x7FFFFFu) ? 0x400000u : 0u);
+    const float r1 = v - __uint_as_float(hi);
+    const uint32_t mid = __float_as_uint(r1) & 0xFFFF0000u;
+    const float r2 = r1 - __uint_as_float(mid);
+    part[0] = (uint16_t)(hi >> 16);
+    part[1] = (uint16_t)(fin ? mid >> 16 : 0u);
+    part[2] = (uint16_t)(fin ? __float_as_uint(r2) >> 16 : 0u);
 }
 
 // y + s_a sum_q t[m][q] B_a[n][q] of token m's adapter a, in fp32; y where it has none.

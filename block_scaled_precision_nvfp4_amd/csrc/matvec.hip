@@ -517,7 +517,7 @@ int launch_nvfp4_lora_matvec(const void* x, int64_t ldx, int64_t M, int64_t N, i
     hipStream_t s = (hipStream_t)hip_stream;
     MvArgs a{(const uint16_t*)x, ldx, M, N, K, {{w_codes, w_scales, w_s_enc}, {}}, rows, y, y_f32, -1, 1, {}};
     a.lora = LoraArgs{M, N, K, (int)r, L, a.x, ldx, adapters, (const uint16_t*)lora_a, (const uint16_t*)lora_b, scales,
-                      workspace, y, N, y, N};
+                      workspace, y, N, y, N, false};
     const int e = launch_lora_down(a.lora, s);
     return e ? e : launch_any<false, true>(a, s);
 }

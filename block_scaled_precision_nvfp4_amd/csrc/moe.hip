@@ -15,8 +15,9 @@ namespace bsq {
 
 // ---------------------------------------------------------------- sort
 
-constexpr int SORT_WAVES = 16, SORT_THREADS = 64 * SORT_WAVES;
+constexpr int SORT_WAVES = 16;
 constexpr int SORT_HIST = 8192;        // counters of a workgroup: its waves' times the experts
+constexpr int SORT_KEEP = 16;          // slots of a lane that stay in registers
 
 struct SortArgs {
     const void* experts;   // ids of 4 or 8 bytes
@@ -29,7 +30,7 @@ struct SortArgs {
     int32_t* positions;
     int32_t* source;
     int32_t* counts;       // [workgroups][E], with several workgroups
-    int64_t chunk;         // slots of a workgroup, a multiple of its threads
+    int64_t mine;          // slots of a wave, one after another, a multiple of 64
 };
 
 // A slot's expert, E for one that is dropped.
@@ -48,13 +49,23 @@ __device__ __forceinline__ uint64_t same_id(int id, int bits) {
     return m;
 }
 
-__global__ __launch_bounds__(SORT_THREADS) void moe_count_kernel(SortArgs a) {
+// A slot's rank among its expert's slots of the wave so far, which next[id] counts; one lane of each expert counts
+// for all (an atomic, of the wave's own counter, only so that it also returns the count before).
+__device__ __forceinline__ int take_rank(int* next, int id, int E, int bits, int lane) {
+    const uint64_t m = same_id(id, bits);
+    const int leader = __builtin_ctzll(m);
+    int at = 0;
+    if (id < E && lane == leader) at = atomicAdd(&next[id], __popcll(m));
+    return __shfl(at, leader) + __popcll(m & ((1ull << lane) - 1));
+}
+
+__global__ __launch_bounds__(64 * SORT_WAVES) void moe_count_kernel(SortArgs a) {
     __shared__ int hist[1024];
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
     __syncthreads();
     const int bits = 32 - __builtin_clz(a.E);
-    const int64_t first = (int64_t)blockIdx.x * a.chunk;
-    for (int64_t c = 0; c < a.chunk; c += blockDim.x) {
+    const int64_t chunk = a.mine * (blockDim.x >> 6), first = (int64_t)blockIdx.x * chunk;
+    for (int64_t c = 0; c < chunk; c += blockDim.x) {
         const int64_t i = first + c + threadIdx.x;
         const int id = i < a.n ? sort_id(a, i) : a.E;
         const uint64_t m = same_id(id, bits);
@@ -64,44 +75,63 @@ __global__ __launch_bounds__(SORT_THREADS) void moe_count_kernel(SortArgs a) {
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
 }
 
-// A workgroup places its chunk of slots: counts of its waves, the slots before it (from the other workgroups'
-// counts), the groups' starts, and then every slot's rank among those of its wave.
-__global__ __launch_bounds__(SORT_THREADS) void moe_place_kernel(SortArgs a) {
+// A workgroup places its waves' slots: their ranks within the wave, the slots before the wave (from the other
+// workgroups' counts and the workgroup's own), and the groups' starts.  KEEP: at most SORT_KEEP slots a lane, whose
+// experts and ranks stay in registers in between; otherwise they are read and counted again.
+template <bool KEEP>
+__global__ __launch_bounds__(64 * SORT_WAVES) void moe_place_kernel(SortArgs a) {
     __shared__ int next[SORT_HIST];                    // [wave][E]: the wave's count, then its next row, of each expert
     __shared__ int start[1024], total[1024], before[1024];
     __shared__ int sums[SORT_WAVES];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, E = a.E;
     const int bits = 32 - __builtin_clz(E);
-    const int64_t mine = a.chunk / waves;              // slots of a wave, one after another
-    const int64_t first = (int64_t)blockIdx.x * a.chunk + wave * mine;
-    for (int i = threadIdx.x; i < waves * E; i += blockDim.x) next[i] = 0;
-    __syncthreads();
-    for (int64_t c = 0; c < mine; c += 64) {
-        const int64_t i = first + c + lane;
-        const int id = i < a.n ? sort_id(a, i) : E;
-        const uint64_t m = same_id(id, bits);
-        if (id < E && lane == __builtin_ctzll(m)) atomicAdd(&next[wave * E + id], __popcll(m));
-    }
-    __syncthreads();
-    // slots of each expert in all, and before this workgroup
-    if (gridDim.x == 1) {
-        for (int e = threadIdx.x; e < E; e += blockDim.x) {
-            int s = 0;
-            for (int w = 0; w < waves; ++w) s += next[w * E + e];
-            total[e] = s;
-            before[e] = 0;
+    const int64_t first = ((int64_t)blockIdx.x * waves + wave) * a.mine;
+    int id[SORT_KEEP], rank[SORT_KEEP];
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int u = 0; u < SORT_KEEP; ++u) {
+            const int64_t i = first + 64 * u + lane;
+            id[u] = 64 * u < a.mine && i < a.n ? sort_id(a, i) : E;
         }
-    } else {
-        for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    }
+    for (int i = threadIdx.x; i < waves * E; i += blockDim.x) next[i] = 0;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) total[e] = before[e] = 0;
+    __syncthreads();
+    if (gridDim.x > 1) {   // an expert's counts dealt to as many threads as there are
+        const int group = 1 << (E > 1 ? 32 - __builtin_clz(E - 1) : 0);   // E <= 1024
+        const int parts = blockDim.x / group > 0 ? blockDim.x / group : 1;
+        for (int e = threadIdx.x % group; e < E; e += blockDim.x) {   // more than one round with parts == 1 only
             int s = 0, b = 0;
-            for (int g = 0; g < (int)gridDim.x; ++g) {
+            const int p = parts > 1 ? threadIdx.x / group : 0;
+#pragma unroll 8
+            for (int g = p; g < (int)gridDim.x; g += parts) {
                 const int v = a.counts[(int64_t)g * E + e];
                 s += v;
-                if (g < (int)blockIdx.x) b += v;
+                b += g < (int)blockIdx.x ? v : 0;
             }
-            total[e] = s;
-            before[e] = b;
+            atomicAdd(&total[e], s);
+            atomicAdd(&before[e], b);
         }
+    }
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int u = 0; u < SORT_KEEP; ++u)
+            if (64 * u < a.mine) rank[u] = take_rank(next + wave * E, id[u], E, bits, lane);
+    } else {
+        for (int64_t c = 0; c < a.mine; c += 64) {
+            const int64_t i = first + c + lane;
+            take_rank(next + wave * E, i < a.n ? sort_id(a, i) : E, E, bits, lane);
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {   // what a wave starts from; the group's start comes on top
+        int at = before[e];
+        for (int w = 0; w < waves; ++w) {
+            const int c = next[w * E + e];
+            next[w * E + e] = at;
+            at += c;
+        }
+        if (gridDim.x == 1) total[e] = at;
     }
     __syncthreads();
     // the groups' starts: a running sum of the padded totals, a stretch of experts after another
@@ -130,26 +160,22 @@ __global__ __launch_bounds__(SORT_THREADS) void moe_place_kernel(SortArgs a) {
         for (int e = threadIdx.x; e < E; e += blockDim.x) a.offsets[e] = start[e];
         if (threadIdx.x == 0) a.offsets[E] = base;
     }
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-        int at = start[e] + before[e];
-        for (int w = 0; w < waves; ++w) {
-            const int c = next[w * E + e];
-            next[w * E + e] = at;
-            at += c;
-        }
-    }
-    __syncthreads();
-    for (int64_t c = 0; c < mine; c += 64) {
-        const int64_t i = first + c + lane;
-        const int id = i < a.n ? sort_id(a, i) : E;
-        const uint64_t m = same_id(id, bits);
-        const int leader = __builtin_ctzll(m);
-        int at = 0;
-        if (id < E && lane == leader) at = atomicAdd(&next[wave * E + id], __popcll(m));
-        at = __shfl(at, leader) + __popcll(m & ((1ull << lane) - 1));
-        if (i < a.n) {
-            a.positions[i] = id < E ? at : -1;
-            if (id < E) a.source[at] = (int32_t)i;
+    auto place = [&](int64_t i, int e, int at) {
+        if (i >= a.n) return;
+        a.positions[i] = e < E ? at : -1;
+        if (e < E) a.source[at] = (int32_t)i;
+    };
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int u = 0; u < SORT_KEEP; ++u)
+            if (64 * u < a.mine)
+                place(first + 64 * u + lane, id[u], id[u] < E ? start[id[u]] + next[wave * E + id[u]] + rank[u] : 0);
+    } else {
+        for (int64_t c = 0; c < a.mine; c += 64) {
+            const int64_t i = first + c + lane;
+            const int e = i < a.n ? sort_id(a, i) : E;
+            const int at = take_rank(next + wave * E, e, E, bits, lane);
+            place(i, e, e < E ? start[e] + at : 0);
         }
     }
     // rows of no slot: the groups' padding, and what lies behind the last group
@@ -161,33 +187,45 @@ __global__ __launch_bounds__(SORT_THREADS) void moe_place_kernel(SortArgs a) {
         a.source[r] = -1;
 }
 
-static int64_t sort_groups(int64_t n, int64_t E, int64_t* chunk) {
-    const int64_t threads = E > SORT_HIST / SORT_WAVES ? SORT_HIST / E * 64 : SORT_THREADS;
-    int64_t c = 4096;
-    while ((n + c - 1) / c > 128) c *= 2;
-    *chunk = c < threads ? threads : c;
-    return n <= 16384 ? 1 : (n + *chunk - 1) / *chunk;
+#ifndef SORT_ONE
+#define SORT_ONE 16384
+#define SORT_MINE 128
+#endif
+// The launch's shape: one workgroup up to 16384 slots, of as many waves as have slots; else several, each wave with
+// 128 slots, more where that would be over 128 workgroups.
+struct SortShape {
+    int64_t groups, mine;
+    int waves;
+};
+
+static SortShape sort_shape(int64_t n, int64_t E) {
+    int waves = SORT_WAVES;
+    while (waves * E > SORT_HIST) waves /= 2;
+    if (n <= SORT_ONE) {
+        while (waves > 1 && waves / 2 * 64 >= n) waves /= 2;
+        const int64_t lanes = 64 * waves;
+        return {1, (n + lanes - 1) / lanes * 64, waves};
+    }
+    int64_t mine = SORT_MINE;
+    while ((n + mine * waves - 1) / (mine * waves) > 128) mine *= 2;
+    return {(n + mine * waves - 1) / (mine * waves), mine, waves};
 }
 
-int64_t moe_sort_counts(int64_t n, int64_t E) {
-    int64_t chunk;
-    return sort_groups(n, E, &chunk) * E;
-}
+int64_t moe_sort_counts(int64_t n, int64_t E) { return sort_shape(n, E).groups * E; }
 
 int launch_moe_sort(const void* experts, int id8, int64_t n, int64_t E, int64_t align, int64_t rows, int64_t* offsets,
                     int32_t* positions, int32_t* source, int32_t* counts, void* hip_stream) {
     hipStream_t s = (hipStream_t)hip_stream;
-    SortArgs a{experts, id8, n, (int)E, (int)align, rows, offsets, positions, source, counts, 0};
-    const int64_t groups = sort_groups(n, E, &a.chunk);
-    int waves = SORT_WAVES;
-    while (waves * E > SORT_HIST) waves /= 2;
-    if (groups == 1) a.chunk = (n + 64 * waves - 1) / (64 * waves) * (64 * waves);
-    if (groups > 1) {
-        hipLaunchKernelGGL(moe_count_kernel, dim3((unsigned)groups), dim3(64 * waves), 0, s, a);
+    const SortShape h = sort_shape(n, E);
+    const SortArgs a{experts, id8, n, (int)E, (int)align, rows, offsets, positions, source, counts, h.mine};
+    const dim3 grid((unsigned)h.groups), block(64 * h.waves);
+    if (h.groups > 1) {
+        hipLaunchKernelGGL(moe_count_kernel, grid, block, 0, s, a);
         const int e = (int)hipGetLastError();
         if (e) return e;
     }
-    hipLaunchKernelGGL(moe_place_kernel, dim3((unsigned)groups), dim3(64 * waves), 0, s, a);
+    if (h.mine <= 64 * SORT_KEEP) hipLaunchKernelGGL(moe_place_kernel<true>, grid, block, 0, s, a);
+    else hipLaunchKernelGGL(moe_place_kernel<false>, grid, block, 0, s, a);
     return (int)hipGetLastError();
 }
 
@@ -535,8 +573,9 @@ struct CombineBwdArgs {
     unsigned token_groups;
 };
 
-// A wave takes a token: its row of dout with each of its slots' rows.
-template <bool YF32>
+// A wave takes a slot: the token's row of dout (which the waves of its other slots read about the same time, so that it
+// comes from memory once) with the slot's row of y, U pieces of 512 elements at a time.
+template <bool YF32, int U>
 __global__ __launch_bounds__(MOE_THREADS) void moe_combine_backward_kernel(CombineBwdArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     if (blockIdx.x >= a.token_groups) {
@@ -547,31 +586,42 @@ __global__ __launch_bounds__(MOE_THREADS) void moe_combine_backward_kernel(Combi
         });
         return;
     }
-    const int64_t t = (int64_t)blockIdx.x * MOE_WAVES + wave;
-    if (t >= a.s.T) return;
-    for (int j = 0; j < a.s.k; ++j) {
-        const int64_t r = a.s.row(t, j);
-        float dot = 0.0f;
-        if (r >= 0) {
-            const float w = a.weights[t * a.s.k + j];
-            for (int64_t c = 8 * lane; c < a.H; c += 512) {
-                float d[8], v[8], o[8];
-                unpack_bf16x8(*(const uint4*)(a.dout + t * a.H + c), d);
-                Row8<YF32> q;
-                q.load(a.y, r * a.H + c);
-                q.values(v);
+    const int64_t i = (int64_t)blockIdx.x * MOE_WAVES + wave;
+    if (i >= a.s.T * a.s.k) return;
+    const int64_t t = i / a.s.k;
+    const int32_t r = a.s.positions[i];
+    if (r < 0 || r >= a.s.rows) {
+        if (lane == 0) a.dweights[i] = 0.0f;
+        return;
+    }
+    const float w = a.weights[i];
+    float dot = 0.0f;
+    for (int64_t c0 = 8 * lane; c0 < a.H; c0 += 512 * U) {
+        uint4 d[U];
+        Row8<YF32> q[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c0 + 512 * u < a.H) {
+                q[u].load(a.y, (int64_t)r * a.H + c0 + 512 * u);
+                d[u] = *(const uint4*)(a.dout + t * a.H + c0 + 512 * u);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c0 + 512 * u < a.H) {
+                float x[8], v[8];
+                unpack_bf16x8(d[u], x);
+                q[u].values(v);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    dot = __builtin_fmaf(d[e], v[e], dot);
-                    o[e] = w * d[e];
+                    dot = __builtin_fmaf(x[e], v[e], dot);
+                    x[e] = w * x[e];
                 }
-                store8<YF32>(a.dy, r * a.H + c, o);
+                store8<YF32>(a.dy, (int64_t)r * a.H + c0 + 512 * u, x);
             }
-        }
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
-        if (lane == 0) a.dweights[t * a.s.k + j] = dot;
     }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
+    if (lane == 0) a.dweights[i] = dot;
 }
 
 int launch_moe_combine_backward(const void* dout, const void* y, int y_f32, int64_t T, int64_t k, int64_t H,
@@ -579,11 +629,11 @@ int launch_moe_combine_backward(const void* dout, const void* y, int y_f32, int6
                                 void* dy, float* dweights, void* hip_stream) {
     if (T * k == 0 && rows == 0) return 0;
     hipStream_t s = (hipStream_t)hip_stream;
-    const unsigned tg = (unsigned)((T + MOE_WAVES - 1) / MOE_WAVES);
+    const unsigned tg = (unsigned)((T * k + MOE_WAVES - 1) / MOE_WAVES);
     const CombineBwdArgs a{(const uint16_t*)dout, y, H, {positions, source, T, (int)k, rows}, weights, dy, dweights, tg};
     const dim3 grid(tg + empty_groups(rows)), block(MOE_THREADS);
-    if (y_f32) hipLaunchKernelGGL((moe_combine_backward_kernel<true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((moe_combine_backward_kernel<false>), grid, block, 0, s, a);
+    if (y_f32) hipLaunchKernelGGL((moe_combine_backward_kernel<true, 2>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((moe_combine_backward_kernel<false, 4>), grid, block, 0, s, a);
     return (int)hipGetLastError();
 }
 

@@ -537,7 +537,7 @@ int clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* n
  * moe_sort -- a stable sort of slots by expert, each expert's rows starting at a multiple of align.
  *   experts    int32 (id_bytes 4) or int64 (8) [slots], device: a slot's expert.  A slot whose id is outside
  *              [0, num_experts) is dropped (an expert that is full, or on another rank).
- *   slots in [0, 2^30], num_experts in [1, 1024], align a power of two up to 256 (BSQ_GROUP_K needs 32).
+ *   slots in [0, 2^25], num_experts in [1, 1024], align a power of two up to 256 (BSQ_GROUP_K needs 32).
  *   rows       rows of the sorted order; at least moe_sort_rows(slots, num_experts, align), which holds any choice of
  *              experts: (slots + min(slots, num_experts) (align - 1)) rounded down to a multiple of align.
  *   offsets    int64[num_experts + 1] (device): the groups' starts; offsets[num_experts] is the end of the last
@@ -559,7 +559,7 @@ int moe_sort(const void* experts, int id_bytes, int64_t slots, int64_t num_exper
  *   x          bf16, token t at x + t * ldx elements; ldx >= width, ldx % 8 == 0.  width % 8 == 0.
  *   positions  int32[tokens][k], source int32[rows] as moe_sort writes them.  Both are read; entries outside their range
  *              count as none, and what is written to a row on which the two disagree is unspecified.
- *   tokens <= 2^23, k <= 64, tokens * ceil(width / 512) <= 2^25.
+ *   tokens <= 2^23, k <= 64, tokens * k <= 2^25, tokens * ceil(width / 512) <= 2^25.
  * moe_gather_nvfp4_rowscaled -- nvfp4_quantize_rowscaled (BSQ_RNE, no transform) of that out, bit for bit, without the
  * copy in between: a token is quantized once and its codes written to its k rows.  width % 16 == 0.
  *   codes [rows][width/2], scales [rows][width/16], s_enc_rows float[rows] (device).
