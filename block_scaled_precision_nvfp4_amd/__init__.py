@@ -93,6 +93,8 @@ def lib():
         L.moe_combine_backward.argtypes = [i64, i64, i64, vp, vp, i32, i64, vp, vp, vp, vp, vp, vp]
         L.lora_workspace_bytes.argtypes = [i64, i64]
         L.lora_workspace_bytes.restype = C.c_int64
+        L.nvfp4_lora_workspace_bytes.argtypes = [i64, i64, i64, i32]
+        L.nvfp4_lora_workspace_bytes.restype = C.c_int64
         L.lora_add.argtypes = [i64, i64, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, i32, vp, vp]
         L.nvfp4_lora_matvec.argtypes = [i32, i64, i64, i64, vp, i64, vp, vp, vp, i64, i64, vp, vp, vp, vp, vp, i32, vp, vp]
         for f in ("moe_sort", "moe_gather", "moe_gather_nvfp4_rowscaled", "moe_gather_mxfp8", "moe_combine",
@@ -758,12 +760,12 @@ def moe_sort(experts: torch.Tensor, num_experts: int, align: int = 1,
         raise ValueError("experts must be [tokens, k]")
     dev, n, L = experts.device, experts.numel(), lib()
     rows, need = L.moe_sort_rows(n, num_experts, align), L.moe_sort_workspace_bytes(n, num_experts)
-    ws = _workspace(workspace, max(need, 0), dev)
+    ws = _workspace(workspace, need, dev) if need > 0 or workspace is not None else None   # few slots need none
     offsets = torch.empty(max(num_experts, 0) + 1, dtype=torch.int64, device=dev)
-    positions = torch.empty(experts.shape, dtype=torch.int32, device=dev)
+    positions = torch.empty_like(experts, dtype=torch.int32)
     source = torch.empty(max(rows, 0), dtype=torch.int32, device=dev)
     _check("moe_sort", L.moe_sort(experts.data_ptr(), experts.element_size(), n, num_experts, align, rows,
-                                  offsets.data_ptr(), positions.data_ptr(), source.data_ptr(), ws.data_ptr(), _stream(dev)))
+                                  offsets.data_ptr(), positions.data_ptr(), source.data_ptr(), _ptr(ws), _stream(dev)))
     return {"offsets": offsets, "positions": positions, "source": source}
 
 
@@ -924,14 +926,15 @@ def nvfp4_lora_matvec(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
                       scales: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
                       out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """``nvfp4_matvec`` with each token's low-rank adapter added before the one rounding of y [M, N]; the adapters as for
-    ``lora_add``."""
+    ``lora_add``.  ``workspace``: lib().nvfp4_lora_workspace_bytes(M, N, rank, OUT_BF16 or OUT_F32) bytes; one is
+    allocated when none is given."""
     M, K, ldx = _tokens(x)
     dev = x.device
     N, rows = _weights(w_codes, w_scales, w_s_enc, K, "w", dev)
     r, n = _adapters(adapters, lora_a, lora_b, scales, M, N, K, dev)
     y_dtype = _type(out_dtype, "out_dtype")
     out = _output(out, (M, N), out_dtype, dev)
-    ws = _workspace(workspace, max(lib().lora_workspace_bytes(M, r), 0), dev)
+    ws = _workspace(workspace, max(lib().nvfp4_lora_workspace_bytes(M, N, r, y_dtype), 0), dev)
     _check("nvfp4_lora_matvec", lib().nvfp4_lora_matvec(
         FMT_B_ROWSCALED if rows else 0, M, N, K, x.data_ptr(), ldx, w_codes.data_ptr(), w_scales.data_ptr(),
         w_s_enc.data_ptr(), r, n, adapters.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(), _ptr(scales), out.data_ptr(),

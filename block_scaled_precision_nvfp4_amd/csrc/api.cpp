@@ -741,7 +741,7 @@ int moe_sort(const void* experts, int id_bytes, int64_t slots, int64_t num_exper
     if (rows < sorted_rows(slots, num_experts, align) || rows > 0x7FFFFFFF)
         return fail(BSQ_ERR_SHAPE, "%s: rows (%lld) must be in [%lld, 2^31)", fn, (long long)rows,
                     (long long)sorted_rows(slots, num_experts, align));
-    if (!offsets || !workspace || (slots > 0 && (!experts || !positions)) || (rows > 0 && !source))
+    if (!offsets || (!workspace && bsq::moe_sort_counts(slots, num_experts) > 0) || (slots > 0 && (!experts || !positions)) || (rows > 0 && !source))
         return fail(BSQ_ERR_NULL, "%s: NULL argument", fn);
     if (unaligned(offsets, 8) || misaligned(workspace) || unaligned(experts, (uintptr_t)id_bytes) || unaligned(positions, 4) ||
         unaligned(source, 4))
@@ -837,6 +837,12 @@ int64_t lora_workspace_bytes(int64_t tokens, int64_t rank) {
     return (tokens + 15) / 16 * 16 * ((rank + 31) / 32 * 32) * 6;   // three bf16 parts of every down product, or fp32
 }
 
+int64_t nvfp4_lora_workspace_bytes(int64_t tokens, int64_t out_features, int64_t rank, int y_dtype) {
+    const int64_t down = lora_workspace_bytes(tokens, rank);
+    if (down < 0 || out_features < 0 || out_features > (int64_t)1 << 27 || bad_type(y_dtype)) return -1;
+    return down + (y_dtype == BSQ_OUT_F32 ? 0 : tokens * out_features * 4);   // the weights' product in fp32, unless y holds it
+}
+
 int lora_add(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t num_adapters, const void* x, int64_t ldx,
              const int32_t* adapters, const void* lora_a, const void* lora_b, const float* scales, const void* y, int64_t ldy,
              void* out, int64_t ldo, int y_dtype, void* workspace, void* hip_stream) {
@@ -871,9 +877,13 @@ int nvfp4_lora_matvec(int flags, int64_t M, int64_t N, int64_t K, const void* x,
     if (st) return st;
     st = lora_check(fn, M, N, K, rank, num_adapters, adapters, lora_a, lora_b, scales, workspace);
     if (st) return st;
+    if (bsq::lora_up_groups(M, N) >= (int64_t)1 << 24)
+        return fail(BSQ_ERR_SHAPE, "%s: %lld tokens by %lld are too large for one launch", fn, (long long)M, (long long)N);
+    float* down = static_cast<float*>(workspace);
     return launched(bsq::launch_nvfp4_lora_matvec(x, ldx, M, N, K, w_codes, w_scales, w_s_enc, flags != 0, rank, num_adapters,
-                                                  adapters, lora_a, lora_b, scales, static_cast<float*>(workspace), y,
-                                                  y_dtype == BSQ_OUT_F32, hip_stream), fn);
+                                                  adapters, lora_a, lora_b, scales, down,
+                                                  down + lora_workspace_bytes(M, rank) / 4, y, y_dtype == BSQ_OUT_F32,
+                                                  hip_stream), fn);
 }
 
 }  // extern "C"

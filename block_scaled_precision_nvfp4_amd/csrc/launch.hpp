@@ -91,7 +91,7 @@ int launch_lora_add(int f32, int64_t M, int64_t N, int64_t K, int64_t r, int64_t
 int launch_nvfp4_lora_matvec(const void* x, int64_t ldx, int64_t M, int64_t N, int64_t K, const uint8_t* w_codes,
                              const uint8_t* w_scales, const float* w_s_enc, int rows, int64_t r, int64_t L,
                              const int32_t* adapters, const void* lora_a, const void* lora_b, const float* scales,
-                             float* workspace, void* y, int y_f32, void* hip_stream);
+                             float* down, float* base, void* y, int y_f32, void* hip_stream);
 const char* hip_error_string(int e);
 
 }  // namespace bsq

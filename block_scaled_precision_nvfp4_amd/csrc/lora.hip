@@ -39,7 +39,7 @@ __device__ __forceinline__ void for_adapters(int ids, int first, int step, F&& b
 constexpr int LORA_PITCH = 144;   // bytes between rows in LDS: the fragments' reads cover all banks
 constexpr int lora_waves(int nr) { return nr == 4 ? 8 : 16; }
 
-template <int NR, bool PARTS>
+template <int NR>
 __global__ __launch_bounds__(64 * lora_waves(NR)) void lora_down_kernel(LoraArgs a) {
     constexpr int W = lora_waves(NR), D = NR == 1 ? 4 : 2, ROWS = LORA_TOKENS * (NR + 1);
     static_assert(W * NR * LORA_TOKENS * 17 * 4 <= W * ROWS * LORA_PITCH, "the join takes the rows' place");
@@ -109,42 +109,52 @@ __global__ __launch_bounds__(64 * lora_waves(NR)) void lora_down_kernel(LoraArgs
             float t = 0.0f;
 #pragma unroll
             for (int u = 0; u < W; ++u) t += red[((u * NR + n) * LORA_TOKENS + m) * 17 + q];
-            if constexpr (PARTS) {
-                if (rank >= a.r) continue;
-                uint16_t p[3];
-                lora_split(t, p);
-                uint16_t* at = (uint16_t*)a.t + ((int64_t)tile * lora_steps(a.r) + rank / 32) * 3 * 512 + (m + 16 * (rank / 8 % 4)) * 8 + rank % 8;
-                at[0] = p[0];
-                at[512] = p[1];
-                at[1024] = p[2];
-            } else if (rank < a.r) {
-                a.t[(m0 + m) * a.r + rank] = t;
-            }
+            if (rank >= a.r) continue;
+            uint16_t p[3];
+            lora_split(t, p);
+            uint16_t* at = (uint16_t*)a.t + ((int64_t)tile * lora_steps(a.r) + rank / 32) * 3 * 512 + (m + 16 * (rank / 8 % 4)) * 8 + rank % 8;
+            at[0] = p[0];
+            at[512] = p[1];
+            at[1024] = p[2];
         }
         __syncthreads();   // before the next adapter's rows
     });
 }
 
-// The up products of 64 columns by a tile of 16 tokens per wave.  The workgroup's waves take neighbouring tiles, which
-// mostly share an adapter: its 64 rows of B come through LDS, whole lines at a time, for all of them.  t comes as the
-// matrix instruction's fragments, in three bf16 parts that add up to it exactly.  Column r16 of block b stands for
-// column 4 r16 + b, so that a lane ends with 4 adjacent columns of each of 4 tokens (4 g + i) and 16 lanes read and
-// write 128 (or 256) adjacent bytes of y.
+template <bool F32>
+__device__ __forceinline__ float lora_y(const LoraArgs& a, int64_t m, int64_t n) {
+    if constexpr (F32) return ((const float*)a.y)[m * a.ldy + n];
+    else return __uint_as_float((uint32_t)((const uint16_t*)a.y)[m * a.ldy + n] << 16);
+}
+
+template <bool F32>
+__device__ __forceinline__ void lora_store(const LoraArgs& a, int64_t m, int64_t n, float v) {
+    if constexpr (F32) ((float*)a.out)[m * a.ldo + n] = v;
+    else ((uint16_t*)a.out)[m * a.ldo + n] = (uint16_t)bf16x2_rne(v, 0.0f);
+}
+
+// The up products of a tile of 16 tokens per wave by `chunks` times 64 columns, one after another.  The workgroup's waves
+// take neighbouring tiles, which mostly share an adapter: its 64 rows of B come through LDS, whole lines at a time,
+// for all of them, the next ones (and y's) asked for before the present ones are used.  t comes as the matrix
+// instruction's fragments, in three bf16 parts that add up to it exactly.  Column r16 of block b stands for column 4 r16 + b,
+// so that a lane ends with 4 adjacent columns of each of 4 tokens (4 g + i) and 16 lanes read and write 128 (or 256)
+// adjacent bytes of y.
 constexpr int LORA_UP_WAVES = 4, LORA_COLS = 64;
 
-// RS: steps of 32 ranks
-template <bool F32, int RS>
-__global__ __launch_bounds__(64 * LORA_UP_WAVES) void lora_up_kernel(LoraArgs a) {
+// YF, OF: y and out are fp32.  RS: steps of 32 ranks.
+template <bool YF, bool OF, int RS>
+__global__ __launch_bounds__(64 * LORA_UP_WAVES) void lora_up_kernel(LoraArgs a, int chunks) {
     constexpr int PITCH = 64 * RS + 16;   // bytes between rows in LDS; the fragments' reads cover all banks
-    __shared__ __attribute__((aligned(16))) uint8_t lds[LORA_COLS * PITCH];
+    constexpr int BV = RS;                // 16-byte pieces of B of a thread: 64 rows of 4 RS pieces for 256
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2][LORA_COLS * PITCH];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int r16 = lane & 15, g = lane >> 4;
-    const int64_t cols = (a.N + LORA_COLS - 1) / LORA_COLS, n0 = blockIdx.x % cols * LORA_COLS;
-    const int64_t tile0 = blockIdx.x / cols * LORA_UP_WAVES, m0 = (tile0 + wave) * LORA_TOKENS;
-    typedef typename std::conditional<F32, float, uint16_t>::type item;
-    typedef typename std::conditional<F32, uint4, uint2>::type vec;
-    const bool whole = n0 + LORA_COLS <= a.N && a.vec;   // else element by element
-    const int64_t c0 = n0 + 4 * r16;
+    const int64_t cols = (a.N + LORA_COLS - 1) / LORA_COLS, groups = (cols + chunks - 1) / chunks;
+    const int64_t first = blockIdx.x % groups * chunks;
+    const int last = (int)(cols - first < chunks ? cols - first : chunks);
+    const int64_t tile0 = blockIdx.x / groups * LORA_UP_WAVES, m0 = (tile0 + wave) * LORA_TOKENS;
+    typedef typename std::conditional<YF, float, uint16_t>::type item;
+    typedef typename std::conditional<YF, uint4, uint2>::type vec;
     const int steps = lora_steps(a.r), cpr = a.r / 8;    // 16-byte pieces of a row of B
     const int64_t ml = tile0 * LORA_TOKENS + lane;       // lane's of the workgroup's 64 tokens
     int all = ml < a.M ? a.adapters[ml] : -1;
@@ -158,137 +168,183 @@ __global__ __launch_bounds__(64 * LORA_UP_WAVES) void lora_up_kernel(LoraArgs a)
             if (32 * q + 8 * g < a.r && m0 < a.M)
                 part[q][p] = *(const bf16x8_t*)((const uint16_t*)a.t + (((tile0 + wave) * steps + q) * 3 + p) * 512 + 8 * lane);
         }
-    vec v[4];
+    auto column = [&](int c) { return (first + c) * LORA_COLS + 4 * r16; };
+    auto whole = [&](int c) { return a.vec && (first + c + 1) * LORA_COLS <= a.N; };   // else element by element
+    vec v[4], vn[4];
+    auto load_y = [&](int c, vec (&d)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (whole && m0 + 4 * g + i < a.M) v[i] = *(const vec*)((const item*)a.y + (m0 + 4 * g + i) * a.ldy + c0);
+        for (int i = 0; i < 4; ++i)
+            if (whole(c) && m0 + 4 * g + i < a.M) d[i] = *(const vec*)((const item*)a.y + (m0 + 4 * g + i) * a.ldy + column(c));
+    };
+    int row[BV], piece[BV];   // of the thread's pieces of B
+#pragma unroll
+    for (int e = 0; e < BV; ++e) {
+        const int at = (int)threadIdx.x + 256 * e;
+        row[e] = at / cpr;
+        piece[e] = at - row[e] * cpr;
+    }
+    uint4 wb[BV];
+    auto load_b = [&](int c, int id) {
+        const int64_t n0 = (first + c) * LORA_COLS;
+#pragma unroll
+        for (int e = 0; e < BV; ++e) {
+            wb[e] = make_uint4(0, 0, 0, 0);
+            if (row[e] < LORA_COLS && n0 + row[e] < a.N)
+                wb[e] = *(const uint4*)(a.b + ((int64_t)id * a.N + n0 + row[e]) * a.r + 8 * piece[e]);
+        }
+    };
+    load_y(0, v);
     int mine[4];   // the adapters of the lane's tokens of y
-#pragma unroll
-    for (int i = 0; i < 4; ++i) mine[i] = __shfl(all, 16 * wave + 4 * g + i);
-    floatx4 add[4];
     float scale[4];
-    for (uint64_t left = __ballot(all >= 0); left != 0;) {   // the same in every wave
-        const int id = __builtin_amdgcn_readlane(all, __builtin_ctzll(left));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        mine[i] = __shfl(all, 16 * wave + 4 * g + i);
+        scale[i] = a.scales && mine[i] >= 0 ? a.scales[mine[i]] : 1.0f;
+    }
+    const uint64_t some = __ballot(all >= 0);   // the same in every wave
+    if (some == 0 && a.out == a.y) return;
+    auto finish = [&](int c, const floatx4 (&add)[4]) {
+        const int64_t c0 = column(c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t m = m0 + 4 * g + i;
+            const bool has = mine[i] >= 0;
+            if (m >= a.M || (!has && a.out == a.y)) continue;
+            if (whole(c)) {
+                float f[4];
+                if constexpr (YF) {
+                    f[0] = __uint_as_float(v[i].x); f[1] = __uint_as_float(v[i].y);
+                    f[2] = __uint_as_float(v[i].z); f[3] = __uint_as_float(v[i].w);
+                } else {
+                    f[0] = bf16_lo(v[i].x); f[1] = bf16_hi(v[i].x);
+                    f[2] = bf16_lo(v[i].y); f[3] = bf16_hi(v[i].y);
+                }
+                if (has)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) f[b] = __builtin_fmaf(scale[i], add[i][b], f[b]);
+                if constexpr (OF) *(float4*)((float*)a.out + m * a.ldo + c0) = make_float4(f[0], f[1], f[2], f[3]);
+                else *(uint2*)((uint16_t*)a.out + m * a.ldo + c0) = make_uint2(bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]));
+                continue;
+            }
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (c0 + b < a.N) {
+                    const float y = lora_y<YF>(a, m, c0 + b);
+                    lora_store<OF>(a, m, c0 + b, has ? __builtin_fmaf(scale[i], add[i][b], y) : y);
+                }
+        }
+    };
+    floatx4 add[4] = {};
+    if (some == 0) {   // no token has one: y goes over
+        for (int c = 0; c < last; ++c) {
+            if (c > 0) load_y(c, v);
+            finish(c, add);
+        }
+        return;
+    }
+    // steps: the adapters of a chunk of columns, then the next chunk
+    uint64_t left = some;
+    int c = 0, id = __builtin_amdgcn_readlane(all, __builtin_ctzll(left)), buf = 0;
+    load_b(0, id);
+    while (true) {
         const uint64_t here = __ballot(all == id);
         left &= ~here;
-        for (int e = threadIdx.x; e < LORA_COLS * cpr; e += 64 * LORA_UP_WAVES) {
-            const int row = e / cpr, piece = e - row * cpr;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (n0 + row < a.N) w = *(const uint4*)(a.b + ((int64_t)id * a.N + n0 + row) * a.r + 8 * piece);
-            *(uint4*)(lds + ((row & 3) * 16 + (row >> 2)) * PITCH + 16 * piece) = w;   // block b's rows side by side
+        const bool ends = left == 0;   // the chunk's last step
+        if (ends) left = some;
+        const int next = __builtin_amdgcn_readlane(all, __builtin_ctzll(left)), nc = ends ? c + 1 : c;
+#pragma unroll
+        for (int e = 0; e < BV; ++e)   // block b's rows side by side
+            if (row[e] < LORA_COLS) *(uint4*)(lds[buf] + ((row[e] & 3) * 16 + (row[e] >> 2)) * PITCH + 16 * piece[e]) = wb[e];
+        if (nc < last) {
+            load_b(nc, next);
+            if (ends) load_y(nc, vn);
         }
-        const float sc = a.scales ? a.scales[id] : 1.0f;
         __syncthreads();
         if ((here >> (16 * wave)) & 0xFFFFu) {
             floatx4 acc[4];
 #pragma unroll
             for (int b = 0; b < 4; ++b) acc[b] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int q = 0; q < RS; ++q)
+            for (int q = 0; q < RS; ++q) {
+                bf16x8_t w[4] = {};
+                if (32 * q + 8 * g < a.r)
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    bf16x8_t w = {};
-                    if (32 * q + 8 * g < a.r) w = *(const bf16x8_t*)(lds + (16 * b + r16) * PITCH + 64 * q + 16 * g);
+                    for (int b = 0; b < 4; ++b) w[b] = *(const bf16x8_t*)(lds[buf] + (16 * b + r16) * PITCH + 64 * q + 16 * g);
 #pragma unroll
-                    for (int p = 2; p >= 0; --p) acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part[q][p], w, acc[b], 0, 0, 0);
-                }
+                for (int p = 2; p >= 0; --p)   // four sums in turn: an instruction does not wait for the one before
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part[q][p], w[b], acc[b], 0, 0, 0);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (mine[i] == id) {
-                    add[i] = floatx4{acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
-                    scale[i] = sc;
-                }
+                if (mine[i] == id) add[i] = floatx4{acc[0][i], acc[1][i], acc[2][i], acc[3][i]};
         }
-        __syncthreads();
-    }
+        if (ends) {
+            finish(c, add);
+            if (nc == last) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + 4 * g + i;
-        const bool has = mine[i] >= 0;
-        if (m >= a.M || (!has && a.out == a.y)) continue;
-        item* out = (item*)a.out + m * a.ldo + c0;
-        if (whole) {
-            if (has) {
-                if constexpr (F32) {
-                    v[i] = make_uint4(__float_as_uint(__builtin_fmaf(scale[i], add[i][0], __uint_as_float(v[i].x))),
-                                      __float_as_uint(__builtin_fmaf(scale[i], add[i][1], __uint_as_float(v[i].y))),
-                                      __float_as_uint(__builtin_fmaf(scale[i], add[i][2], __uint_as_float(v[i].z))),
-                                      __float_as_uint(__builtin_fmaf(scale[i], add[i][3], __uint_as_float(v[i].w))));
-                } else {
-                    v[i] = make_uint2(bf16x2_rne(__builtin_fmaf(scale[i], add[i][0], bf16_lo(v[i].x)),
-                                                 __builtin_fmaf(scale[i], add[i][1], bf16_hi(v[i].x))),
-                                      bf16x2_rne(__builtin_fmaf(scale[i], add[i][2], bf16_lo(v[i].y)),
-                                                 __builtin_fmaf(scale[i], add[i][3], bf16_hi(v[i].y))));
-                }
-            }
-            *(vec*)out = v[i];
-            continue;
+            for (int i = 0; i < 4; ++i) v[i] = vn[i];
         }
-        const item* y = (const item*)a.y + m * a.ldy + c0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            if (c0 + b >= a.N) continue;
-            item o = y[b];
-            if (has) {
-                if constexpr (F32) o = __builtin_fmaf(scale[i], add[i][b], o);
-                else o = (uint16_t)bf16x2_rne(__builtin_fmaf(scale[i], add[i][b], __uint_as_float((uint32_t)o << 16)), 0.0f);
-            }
-            out[b] = o;
-        }
+        c = nc;
+        id = next;
+        buf ^= 1;
     }
 }
 
 // Few tokens: a thread takes one value of y, so that any mixture of adapters goes at once.
-constexpr int LORA_FEW = 64;
-
-template <bool F32>
+template <bool YF, bool OF>
 __global__ __launch_bounds__(256) void lora_up_few_kernel(LoraArgs a) {
     const int64_t m = blockIdx.y, n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (n >= a.N) return;
-    if constexpr (F32) {
-        ((float*)a.out)[m * a.ldo + n] = lora_added(a, m, n, ((const float*)a.y)[m * a.ldy + n]);
-    } else {
-        const uint16_t y = ((const uint16_t*)a.y)[m * a.ldy + n];
-        const int id = a.adapters[m];
-        ((uint16_t*)a.out)[m * a.ldo + n] =
-            id < 0 || id >= a.L ? y : (uint16_t)bf16x2_rne(lora_added(a, m, n, __uint_as_float((uint32_t)y << 16)), 0.0f);
-    }
+    const int id = a.adapters[m];
+    if (n < a.N && (a.out != a.y || (id >= 0 && id < a.L))) lora_store<OF>(a, m, n, lora_added(a, m, n, lora_y<YF>(a, m, n)));
 }
 
-template <bool PARTS>
-static int launch_down(const LoraArgs& a, hipStream_t s) {
+__global__ __launch_bounds__(256) void lora_down_few_kernel(LoraArgs a, int rq) {
+    lora_down_few(a, rq, (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)));
+}
+
+int launch_lora_down_many(const LoraArgs& a, hipStream_t s) {
     const int64_t tiles = (a.M + LORA_TOKENS - 1) / LORA_TOKENS;
     // a workgroup for each adapter that a tile can have while the tiles are few
-    const unsigned many = tiles <= 16 ? (unsigned)(a.M < LORA_TOKENS ? a.M : LORA_TOKENS) : 1u;
+    const unsigned many = tiles <= 16 ? LORA_TOKENS : tiles < 256 ? (unsigned)(256 / tiles) : 1u;
     if (a.r <= 16)
-        hipLaunchKernelGGL((lora_down_kernel<1, PARTS>), dim3((unsigned)tiles, many, 1), dim3(64 * lora_waves(1)), 0, s, a);
+        hipLaunchKernelGGL((lora_down_kernel<1>), dim3((unsigned)tiles, many, 1), dim3(64 * lora_waves(1)), 0, s, a);
     else if (a.r <= 32)
-        hipLaunchKernelGGL((lora_down_kernel<2, PARTS>), dim3((unsigned)tiles, many, 1), dim3(64 * lora_waves(2)), 0, s, a);
+        hipLaunchKernelGGL((lora_down_kernel<2>), dim3((unsigned)tiles, many, 1), dim3(64 * lora_waves(2)), 0, s, a);
     else
-        hipLaunchKernelGGL((lora_down_kernel<4, PARTS>), dim3((unsigned)tiles, many, (unsigned)((a.r + 63) / 64)),
+        hipLaunchKernelGGL((lora_down_kernel<4>), dim3((unsigned)tiles, many, (unsigned)((a.r + 63) / 64)),
                            dim3(64 * lora_waves(4)), 0, s, a);
     return (int)hipGetLastError();
 }
-
-int launch_lora_down(const LoraArgs& a, hipStream_t s) { return launch_down<false>(a, s); }
 
 int64_t lora_up_groups(int64_t M, int64_t N) {
     const int64_t tokens = LORA_TOKENS * LORA_UP_WAVES;
     return ((M + tokens - 1) / tokens) * ((N + LORA_COLS - 1) / LORA_COLS);
 }
 
-template <bool F32>
+template <bool YF, bool OF>
 static int launch_up(const LoraArgs& a, hipStream_t s) {
     if (a.M <= LORA_FEW) {
-        hipLaunchKernelGGL((lora_up_few_kernel<F32>), dim3((unsigned)((a.N + 255) / 256), (unsigned)a.M), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((lora_up_few_kernel<YF, OF>), dim3((unsigned)((a.N + 255) / 256), (unsigned)a.M), dim3(256), 0, s, a);
         return (int)hipGetLastError();
     }
-    const dim3 grid((unsigned)lora_up_groups(a.M, a.N)), block(64 * LORA_UP_WAVES);
-    if (a.r <= 32) hipLaunchKernelGGL((lora_up_kernel<F32, 1>), grid, block, 0, s, a);
-    else if (a.r <= 64) hipLaunchKernelGGL((lora_up_kernel<F32, 2>), grid, block, 0, s, a);
-    else if (a.r <= 128) hipLaunchKernelGGL((lora_up_kernel<F32, 4>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((lora_up_kernel<F32, 8>), grid, block, 0, s, a);
+    const int64_t cols = (a.N + LORA_COLS - 1) / LORA_COLS, tiles = lora_up_groups(a.M, LORA_COLS);
+    // as many columns a workgroup as leave two of them for each CU (one where its registers have room for no more):
+    // all run at once, and a workgroup's way in is spread over its columns.  4096 tokens x 4096, rank 64, us:
+    // 4096 workgroups of 64 columns 37, 2048 29, 1024 25, 512 23, 256 32.
+    const int64_t room = a.r > 128 ? 256 : 512;
+    int64_t chunks = (tiles * cols + room - 1) / room;
+    if (chunks > cols) chunks = cols;
+    const dim3 grid((unsigned)(tiles * ((cols + chunks - 1) / chunks))), block(64 * LORA_UP_WAVES);
+    if (a.r <= 32) hipLaunchKernelGGL((lora_up_kernel<YF, OF, 1>), grid, block, 0, s, a, (int)chunks);
+    else if (a.r <= 64) hipLaunchKernelGGL((lora_up_kernel<YF, OF, 2>), grid, block, 0, s, a, (int)chunks);
+    else if (a.r <= 128) hipLaunchKernelGGL((lora_up_kernel<YF, OF, 4>), grid, block, 0, s, a, (int)chunks);
+    else hipLaunchKernelGGL((lora_up_kernel<YF, OF, 8>), grid, block, 0, s, a, (int)chunks);
     return (int)hipGetLastError();
+}
+
+int launch_lora_up(const LoraArgs& a, int y_f32, int out_f32, hipStream_t s) {
+    return !y_f32 ? launch_up<false, false>(a, s) : out_f32 ? launch_up<true, true>(a, s) : launch_up<true, false>(a, s);
 }
 
 int launch_lora_add(int f32, int64_t M, int64_t N, int64_t K, int64_t r, int64_t L, const void* x, int64_t ldx,
@@ -300,9 +356,15 @@ int launch_lora_add(int f32, int64_t M, int64_t N, int64_t K, int64_t r, int64_t
                      scales, workspace, y, ldy, out, ldo,
                      (((uintptr_t)y | (uintptr_t)out | (uintptr_t)(ldy * (f32 ? 4 : 2)) | (uintptr_t)(ldo * (f32 ? 4 : 2))) &
                       (f32 ? 15 : 7)) == 0};
-    const int e = M <= LORA_FEW ? launch_down<false>(a, s) : launch_down<true>(a, s);
-    if (e) return e;
-    return f32 ? launch_up<true>(a, s) : launch_up<false>(a, s);
+    int e;
+    if (M <= LORA_FEW) {
+        const int rq = lora_few_rows(M, a.r);
+        hipLaunchKernelGGL(lora_down_few_kernel, dim3((unsigned)((lora_few_units(M, a.r, rq) + 3) / 4)), dim3(256), 0, s, a, rq);
+        e = (int)hipGetLastError();
+    } else {
+        e = launch_lora_down_many(a, s);
+    }
+    return e ? e : launch_lora_up(a, f32, f32, s);
 }
 
 }  // namespace bsq

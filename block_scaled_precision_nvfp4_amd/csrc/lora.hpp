@@ -25,8 +25,6 @@ struct LoraArgs {
     bool vec;                   // 4 columns of y and out are one aligned access, from every 4th on
 };
 
-int launch_lora_down(const LoraArgs& a, hipStream_t s);
-
 __host__ __device__ constexpr int lora_steps(int r) { return (r + 31) / 32; }
 
 // A value as three bf16 parts that add up to it exactly (8 bits of the significand each, cut, not rounded, so that a
@@ -42,6 +40,68 @@ __device__ __forceinline__ void lora_split(float v, uint16_t (&part)[3]) {
     part[1] = (uint16_t)(fin ? mid >> 16 : 0u);
     part[2] = (uint16_t)(fin ? __float_as_uint(r2) >> 16 : 0u);
 }
+
+// Few tokens: a wave takes a token's products with RQ rows of its adapter's A, U pieces of 512 elements at a time, all
+// their loads in flight at once: t[m][q] as fp32.  Unit `unit` of lora_few_units, 64 lanes.
+constexpr int LORA_FEW = 64;   // tokens at most
+
+__host__ __device__ inline int64_t lora_few_units(int64_t M, int r, int rq) { return M * ((r + rq - 1) / rq); }
+// a wave for every product while that leaves the chip room: the shortest way through K
+__host__ __device__ inline int lora_few_rows(int64_t M, int r) { return M * r <= 2048 ? 1 : 4; }
+
+template <int RQ, int U>
+__device__ __forceinline__ void lora_down_few_rows(const LoraArgs& a, int64_t unit) {
+    const int lane = threadIdx.x & 63, blocks = (a.r + RQ - 1) / RQ, K = (int)a.K;
+    const int64_t m = unit / blocks;
+    const int q0 = (int)(unit % blocks) * RQ;
+    if (m >= a.M) return;
+    const int id = a.adapters[m];
+    if (id < 0 || id >= a.L) return;
+    const uint16_t* x = a.x + m * a.ldx;
+    const uint16_t* w = a.a + ((int64_t)id * a.r + q0) * a.K;   // r is a multiple of RQ
+    float acc[RQ] = {};
+    for (int k0 = 8 * lane; k0 < K; k0 += 512 * U) {
+        uint4 xv[U], wv[RQ][U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool in = k0 + 512 * u < K;
+            xv[u] = make_uint4(0, 0, 0, 0);
+            if (in) xv[u] = *(const uint4*)(x + k0 + 512 * u);
+#pragma unroll
+            for (int q = 0; q < RQ; ++q) {
+                wv[q][u] = make_uint4(0, 0, 0, 0);
+                if (in) wv[q][u] = *(const uint4*)(w + (int64_t)q * a.K + k0 + 512 * u);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float f[8];
+            unpack_bf16x8(xv[u], f);
+#pragma unroll
+            for (int q = 0; q < RQ; ++q) {
+                float v[8];
+                unpack_bf16x8(wv[q][u], v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[q] = __builtin_fmaf(f[e], v[e], acc[q]);
+            }
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < RQ; ++q) {
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) acc[q] += __shfl_xor(acc[q], o);
+        if (lane == 0) a.t[m * a.r + q0 + q] = acc[q];
+    }
+}
+
+__device__ __forceinline__ void lora_down_few(const LoraArgs& a, int rq, int64_t unit) {
+    if (rq == 1) lora_down_few_rows<1, 4>(a, unit);
+    else lora_down_few_rows<4, 2>(a, unit);
+}
+
+// Both in lora.hip: the down products of any number of tokens, and the up products onto y.
+int launch_lora_down_many(const LoraArgs& a, hipStream_t s);
+int launch_lora_up(const LoraArgs& a, int y_f32, int out_f32, hipStream_t s);
 
 // y + s_a sum_q t[m][q] B_a[n][q] of token m's adapter a, in fp32; y where it has none.
 __device__ __forceinline__ float lora_added(const LoraArgs& a, int64_t m, int64_t n, float y) {

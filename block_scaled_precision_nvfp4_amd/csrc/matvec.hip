@@ -52,7 +52,9 @@ struct MvArgs {
     int y_f32;
     int act;
     int wr;               // 16-row blocks of a workgroup; its waves are wr times as many as parts of K
-    LoraArgs lora;        // the tokens' adapters, for the kernels that add their products
+    LoraArgs lora;        // the tokens' adapters, for the kernels that take their down products along
+    int downs;            // workgroups of a row of the grid that do, before the others
+    int down_waves, rq;   // their waves at work; lora_down_few
 };
 
 // One lane's 64 elements of a weight row: their codes and the bytes of their 4 block scales.
@@ -157,13 +159,13 @@ __device__ __forceinline__ uint32_t mv_word(const MvPiece& p) {
 
 // The workgroup's outputs from the sums of its parts of K.  sum(o, q, b, m, n): operand o's sum of part q,
 // row block b, token m, row n of the block.  s0: the tensor scales of this thread's first output.
-template <bool GATED, bool LORA, class S>
-__device__ __forceinline__ void mv_join(const MvArgs& a, int parts, int tokens, int64_t m0,
+template <bool GATED, class S>
+__device__ __forceinline__ void mv_join(const MvArgs& a, int64_t bx, int parts, int tokens, int64_t m0,
                                         const float (&s0)[GATED ? 2 : 1], S&& sum) {
     constexpr int NW = GATED ? 2 : 1;
     for (int i = threadIdx.x; i < tokens * MV_ROWS * a.wr; i += blockDim.x) {
         const int nt = i % MV_ROWS, b = i / MV_ROWS % a.wr, mt = i / MV_ROWS / a.wr;
-        const int64_t m = m0 + mt, n = ((int64_t)blockIdx.x * a.wr + b) * MV_ROWS + nt;
+        const int64_t m = m0 + mt, n = (bx * a.wr + b) * MV_ROWS + nt;
         if (n >= a.N) continue;
         float v[NW];
 #pragma unroll
@@ -175,7 +177,6 @@ __device__ __forceinline__ void mv_join(const MvArgs& a, int parts, int tokens, 
         float y = v[0];
         if constexpr (GATED)
             y = (a.act == 0 ? act_value<0>(v[0]) : a.act == 1 ? act_value<1>(v[0]) : act_value<2>(v[0])) * v[NW - 1];
-        if constexpr (LORA) y = lora_added(a.lora, m, n, y);
         if (a.y_f32) ((float*)a.y)[m * a.N + n] = y;
         else ((uint16_t*)a.y)[m * a.N + n] = (uint16_t)bf16x2_rne(y, 0.0f);
     }
@@ -183,10 +184,26 @@ __device__ __forceinline__ void mv_join(const MvArgs& a, int parts, int tokens, 
 
 // Those tensor scales, fetched at the start: at the end they would cost a trip to memory.
 template <int NW>
-__device__ __forceinline__ void mv_scales(const MvArgs& a, float (&s0)[NW]) {
-    const int64_t n = ((int64_t)blockIdx.x * a.wr + threadIdx.x / MV_ROWS % a.wr) * MV_ROWS + threadIdx.x % MV_ROWS;
+__device__ __forceinline__ void mv_scales(const MvArgs& a, int64_t bx, float (&s0)[NW]) {
+    const int64_t n = (bx * a.wr + threadIdx.x / MV_ROWS % a.wr) * MV_ROWS + threadIdx.x % MV_ROWS;
 #pragma unroll
     for (int o = 0; o < NW; ++o) s0[o] = a.w[o].s_enc[a.rows ? (n < a.N ? n : a.N - 1) : 0];
+}
+
+// The adapters' down products of the tokens, which have nothing to do with the weights: some workgroups take them
+// while the others stream the weights, so that they cost no launch.  Returns whether this workgroup did.
+__device__ __forceinline__ bool mv_down(const MvArgs& a) {
+    if (blockIdx.x >= (unsigned)a.downs) return false;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    if (wave < a.down_waves)
+        lora_down_few(a.lora, a.rq, ((int64_t)blockIdx.y * a.downs + blockIdx.x) * a.down_waves + wave);
+    return true;
+}
+
+// The workgroup's place among those that take the weights.
+template <bool LORA>
+__device__ __forceinline__ int64_t mv_block(const MvArgs& a) {
+    return LORA ? (int64_t)blockIdx.x - a.downs : (int64_t)blockIdx.x;
 }
 
 // ---------------------------------------------------------------- one token
@@ -251,10 +268,12 @@ template <bool GATED, int LOAD, bool LORA>
 __global__ __launch_bounds__(64 * MV_ONE_WAVES) void matvec_kernel(MvArgs a) {
     constexpr int NW = GATED ? 2 : 1, D = 4 / NW;   // chunks in flight
     __shared__ float red[MV_ONE_WAVES][NW][4][MV_ROWS + 1];
+    if (LORA && mv_down(a)) return;
+    const int64_t bx = mv_block<LORA>(a);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int parts = (int)(blockDim.x >> 6);
     const int r16 = lane & 15, g = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * MV_ROWS, m0 = blockIdx.y;
+    const int64_t n0 = bx * MV_ROWS, m0 = blockIdx.y;
     const uint32_t K = (uint32_t)a.K;
     const int chunks = (int)((K + MV_CHUNK - 1) / MV_CHUNK);
     const __amdgpu_buffer_rsrc_t xr =
@@ -267,7 +286,7 @@ __global__ __launch_bounds__(64 * MV_ONE_WAVES) void matvec_kernel(MvArgs a) {
         acc[o] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     }
     float s0[NW];
-    mv_scales(a, s0);
+    mv_scales(a, bx, s0);
     MvPiece p[D][NW];
     MvOneX x[D];
     auto load = [&](int c, int d) {
@@ -314,7 +333,7 @@ __global__ __launch_bounds__(64 * MV_ONE_WAVES) void matvec_kernel(MvArgs a) {
 #pragma unroll
     for (int o = 0; o < NW; ++o) red[wave][o][g][r16] = (acc[o][0] + acc[o][1]) + (acc[o][2] + acc[o][3]);
     __syncthreads();
-    mv_join<GATED, LORA>(a, parts, 1, m0, s0, [&](int o, int q, int, int, int n) {
+    mv_join<GATED>(a, bx, parts, 1, m0, s0, [&](int o, int q, int, int, int n) {
         const float (&f)[4][MV_ROWS + 1] = red[q][o];
         return (f[0][n] + f[1][n]) + (f[2][n] + f[3][n]);
     });
@@ -338,10 +357,12 @@ __global__ __launch_bounds__(64 * mv_waves(T)) void matvec_tokens_kernel(MvArgs 
     constexpr int XBUF = mv_parts(T) * T * MV_XPITCH;
     static_assert(mv_waves(T) * NW * T * RS * 4 <= 2 * XBUF, "the join takes the tokens' place");
     __shared__ __attribute__((aligned(16))) uint8_t lds[2 * XBUF];
+    if (LORA && mv_down(a)) return;
+    const int64_t bx = mv_block<LORA>(a);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int parts = (int)(blockDim.x >> 6) / a.wr, wr = wave % a.wr, part = wave / a.wr;
     const int r16 = lane & 15, g = lane >> 4;
-    const int64_t n0 = ((int64_t)blockIdx.x * a.wr + wr) * MV_ROWS, m0 = (int64_t)blockIdx.y * T;
+    const int64_t n0 = (bx * a.wr + wr) * MV_ROWS, m0 = (int64_t)blockIdx.y * T;
     const int tokens = (int)(a.M - m0 < T ? a.M - m0 : T);
     const uint32_t K = (uint32_t)a.K;
     const int steps = (int)((K + MV_CHUNK * parts - 1) / (MV_CHUNK * parts));
@@ -349,7 +370,7 @@ __global__ __launch_bounds__(64 * mv_waves(T)) void matvec_tokens_kernel(MvArgs 
 #pragma unroll
     for (int o = 0; o < NW; ++o) w[o] = mv_rsrc(a.w[o], n0, a.N, a.K, r16);
     float s0[NW];
-    mv_scales(a, s0);
+    mv_scales(a, bx, s0);
     floatx4 acc[NW][MT];
 #pragma unroll
     for (int o = 0; o < NW; ++o)
@@ -437,12 +458,21 @@ __global__ __launch_bounds__(64 * mv_waves(T)) void matvec_tokens_kernel(MvArgs 
                 if (m < tokens) red[((wave * NW + o) * T + m) * RS + r16] = acc[o][t][r];
             }
     __syncthreads();
-    mv_join<GATED, LORA>(a, parts, tokens, m0, s0, [&](int o, int q, int b, int m, int n) {
+    mv_join<GATED>(a, bx, parts, tokens, m0, s0, [&](int o, int q, int b, int m, int n) {
         return red[(((q * a.wr + b) * NW + o) * T + m) * RS + n];
     });
 }
 
 // ---------------------------------------------------------------- launches
+
+// The workgroups that the down products take of each of `rows` rows of the grid.  Beside one token, and up to four, a
+// wave takes one row of A, and four share a workgroup, which finds room on any CU.  The kernels of more tokens
+// have a CU's LDS to themselves: few workgroups, of four rows a wave, that go to the CUs the weights leave idle.
+static void mv_downs(MvArgs& a, int64_t waves, int64_t rows) {
+    a.rq = a.M <= 4 ? 1 : 4;
+    a.down_waves = (int)(a.M <= 4 && waves > 4 ? 4 : waves);
+    a.downs = (int)((lora_few_units(a.M, a.lora.r, a.rq) + a.down_waves * rows - 1) / (a.down_waves * rows));
+}
 
 // One token: as many waves share K as let every workgroup be resident at once (16 waves on each CU), at least
 // 4 and no more than there are chunks.
@@ -453,7 +483,8 @@ static int launch_one(MvArgs a, hipStream_t s) {
     while (parts > 4 && parts * blocks * a.M > MV_CUS * MV_ONE_WAVES) parts /= 2;
     while (parts > 1 && parts / 2 >= chunks) parts /= 2;
     a.wr = 1;
-    hipLaunchKernelGGL((matvec_kernel<GATED, LOAD, LORA>), dim3((unsigned)blocks, (unsigned)a.M), dim3(64 * parts), 0, s, a);
+    if (LORA) mv_downs(a, parts, a.M);
+    hipLaunchKernelGGL((matvec_kernel<GATED, LOAD, LORA>), dim3((unsigned)(a.downs + blocks), (unsigned)a.M), dim3(64 * parts), 0, s, a);
     return (int)hipGetLastError();
 }
 
@@ -472,7 +503,8 @@ static int launch_tokens(MvArgs a, hipStream_t s) {
     while (a.wr < 4 && a.wr * MV_CUS < blocks * mb) a.wr *= 2;
     int parts = mv_waves(T) / a.wr < mv_parts(T) ? mv_waves(T) / a.wr : mv_parts(T);
     while (parts > 1 && parts / 2 >= chunks) parts /= 2;
-    hipLaunchKernelGGL((matvec_tokens_kernel<T, GATED, LOAD, LORA>), dim3((unsigned)((blocks + a.wr - 1) / a.wr), (unsigned)mb),
+    if (LORA) mv_downs(a, a.wr * parts, mb);
+    hipLaunchKernelGGL((matvec_tokens_kernel<T, GATED, LOAD, LORA>), dim3((unsigned)(a.downs + (blocks + a.wr - 1) / a.wr), (unsigned)mb),
                        dim3(64 * a.wr * parts), 0, s, a);
     return (int)hipGetLastError();
 }
@@ -504,22 +536,30 @@ int launch_nvfp4_matvec(int act, const void* x, int64_t ldx, int64_t M, int64_t 
                         void* hip_stream) {
     if (M == 0 || N == 0) return 0;
     const MvArgs a{(const uint16_t*)x, ldx, M, N, K, {{w_codes, w_scales, w_s_enc}, {up_codes, up_scales, up_s_enc}},
-                   rows, y, y_f32, act, 1, {}};
+                   rows, y, y_f32, act, 1, {}, 0, 0, 0};
     hipStream_t s = (hipStream_t)hip_stream;
     return act < 0 ? launch_any<false, false>(a, s) : launch_any<true, false>(a, s);
 }
 
+// The weights' product in fp32 (y itself, or in `base`) with the down products beside it, then the up products.
 int launch_nvfp4_lora_matvec(const void* x, int64_t ldx, int64_t M, int64_t N, int64_t K, const uint8_t* w_codes,
                              const uint8_t* w_scales, const float* w_s_enc, int rows, int64_t r, int64_t L,
                              const int32_t* adapters, const void* lora_a, const void* lora_b, const float* scales,
-                             float* workspace, void* y, int y_f32, void* hip_stream) {
+                             float* down, float* base, void* y, int y_f32, void* hip_stream) {
     if (M == 0 || N == 0) return 0;
     hipStream_t s = (hipStream_t)hip_stream;
-    MvArgs a{(const uint16_t*)x, ldx, M, N, K, {{w_codes, w_scales, w_s_enc}, {}}, rows, y, y_f32, -1, 1, {}};
+    void* sum = y_f32 ? y : base;
+    MvArgs a{(const uint16_t*)x, ldx, M, N, K, {{w_codes, w_scales, w_s_enc}, {}}, rows, sum, 1, -1, 1, {}, 0, 0, 0};
     a.lora = LoraArgs{M, N, K, (int)r, L, a.x, ldx, adapters, (const uint16_t*)lora_a, (const uint16_t*)lora_b, scales,
-                      workspace, y, N, y, N, false};
-    const int e = launch_lora_down(a.lora, s);
-    return e ? e : launch_any<false, true>(a, s);
+                      down, sum, N, y, N, N % 4 == 0};
+    int e;
+    if (M <= LORA_FEW) {
+        e = launch_any<false, true>(a, s);
+    } else {
+        e = launch_lora_down_many(a.lora, s);
+        if (!e) e = launch_any<false, false>(a, s);
+    }
+    return e ? e : launch_lora_up(a.lora, 1, y_f32, s);
 }
 
 }  // namespace bsq

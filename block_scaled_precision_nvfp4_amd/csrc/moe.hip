@@ -187,12 +187,12 @@ __global__ __launch_bounds__(64 * SORT_WAVES) void moe_place_kernel(SortArgs a) 
         a.source[r] = -1;
 }
 
-#ifndef SORT_ONE
-#define SORT_ONE 16384
-#define SORT_MINE 128
-#endif
-// The launch's shape: one workgroup up to 16384 slots, of as many waves as have slots; else several, each wave with
-// 128 slots, more where that would be over 128 workgroups.
+// The launch's shape: one workgroup up to 4096 slots, of as many waves as have slots; else a count first, and
+// several workgroups, each wave with 64 slots or, where that would be over 128 workgroups, more.  us in a graph, one
+// workgroup and several, 8 / 128 experts: 2048 slots 6.1 / 7.7 and 8.2 / 9.3, 4096 7.5 / 9.8 and 8.2 / 9.1 (a
+// second launch costs the host 2), 16384 16.2 / 22.1 and 8.4 / 9.6; with 128 slots a wave 9.5 / 11.1.
+constexpr int SORT_ONE = 4096, SORT_MINE = 64;
+
 struct SortShape {
     int64_t groups, mine;
     int waves;
@@ -211,7 +211,10 @@ static SortShape sort_shape(int64_t n, int64_t E) {
     return {(n + mine * waves - 1) / (mine * waves), mine, waves};
 }
 
-int64_t moe_sort_counts(int64_t n, int64_t E) { return sort_shape(n, E).groups * E; }
+int64_t moe_sort_counts(int64_t n, int64_t E) {
+    const int64_t groups = sort_shape(n, E).groups;
+    return groups > 1 ? groups * E : 0;
+}
 
 int launch_moe_sort(const void* experts, int id8, int64_t n, int64_t E, int64_t align, int64_t rows, int64_t* offsets,
                     int32_t* positions, int32_t* source, int32_t* counts, void* hip_stream) {

@@ -545,7 +545,8 @@ int clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* n
  *   positions  int32[slots] (device): each slot's row, -1 for a dropped one.
  *   source     int32[rows] (device): each row's slot, -1 for a row without one (padding, and what lies behind
  *              the last group).
- *   workspace  device scratch of moe_sort_workspace_bytes(slots, num_experts) bytes, as for nvfp4_quantize.
+ *   workspace  device scratch of moe_sort_workspace_bytes(slots, num_experts) bytes (0 for few slots; then it may be
+ *              NULL), as for nvfp4_quantize.
  * The size queries return -1 for sizes out of range.
  */
 int64_t moe_sort_rows(int64_t slots, int64_t num_experts, int64_t align);
@@ -599,7 +600,8 @@ int moe_combine_backward(int64_t tokens, int64_t k, int64_t width, const void* d
  *   adapters   int32[M] (device); outside [0, num_adapters): the token has none and gets y as it is.
  *   lora_a     [num_adapters][rank][K], lora_b [num_adapters][N][rank] bf16; rank a multiple of 8 up to 256
  *              (smaller ones are padded with zeros).  scales float[num_adapters] (device), or NULL: 1.
- *   workspace  device scratch of lora_workspace_bytes(M, rank) bytes, as for nvfp4_quantize.
+ *   workspace  device scratch of lora_workspace_bytes(M, rank) or nvfp4_lora_workspace_bytes(M, N, rank, y_dtype) bytes,
+ *              as for nvfp4_quantize.
  * Products of bf16 values are exact and added up in fp32; the result is rounded once, to y's type.  A NaN or an infinity
  * in a token reaches that token's outputs only, one in an adapter the tokens that have it.  Tokens of one adapter should
  * stand together where there are many: an adapter is read once for every 16 tokens among which it occurs.
@@ -607,12 +609,13 @@ int moe_combine_backward(int64_t tokens, int64_t k, int64_t width, const void* d
  * lora_add -- beside any projection, whose output y is given.
  *   y, out     bf16 or fp32 (y_dtype), rows ldy and ldo elements apart (a projection's slice of a wider output); out
  *              is y itself with ldo == ldy (in place), or overlaps no other argument.  Aligned to their elements.
- *   K % 8 == 0, K < 2^24; M <= 2^20; N any with ceil(M / 16) ceil(N / 256) < 2^24.
+ *   K % 8 == 0, K < 2^24; M <= 2^20; N any with ceil(M / 64) ceil(N / 64) < 2^24.
  *
- * nvfp4_lora_matvec -- beside NVFP4 weights that all tokens share: nvfp4_matvec's arguments and sizes, and its product
- * with the adapters' added in fp32 before the one rounding of y.
+ * nvfp4_lora_matvec -- beside NVFP4 weights that all tokens share: nvfp4_matvec's arguments, and its product with the
+ * adapters' added in fp32 before the one rounding of y.  M and N as for both.
  */
 int64_t lora_workspace_bytes(int64_t tokens, int64_t rank);
+int64_t nvfp4_lora_workspace_bytes(int64_t tokens, int64_t out_features, int64_t rank, int y_dtype);
 int lora_add(int64_t M, int64_t N, int64_t K, int64_t rank, int64_t num_adapters, const void* x, int64_t ldx,
              const int32_t* adapters, const void* lora_a, const void* lora_b, const float* scales, const void* y,
              int64_t ldy, void* out, int64_t ldo, int y_dtype, void* workspace, void* hip_stream);

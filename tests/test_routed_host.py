@@ -33,7 +33,7 @@ SORT["rows"] = (64 + 8 * 31) // 32 * 32
 @pytest.mark.parametrize("kw,status", [
     (dict(id_bytes=2), 3), (dict(slots=-1), 2), (dict(slots=(1 << 25) + 1), 2), (dict(E=0), 2), (dict(E=1025), 2),
     (dict(align=0), 3), (dict(align=24), 3), (dict(align=512), 3), (dict(rows=SORT["rows"] - 1), 2), (dict(rows=1 << 31), 2),
-    (dict(experts=None), 1), (dict(offsets=None), 1), (dict(positions=None), 1), (dict(source=None), 1), (dict(ws=None), 1),
+    (dict(experts=None), 1), (dict(offsets=None), 1), (dict(positions=None), 1), (dict(source=None), 1), (dict(ws=None, slots=8192, rows=1 << 20), 1),
     (dict(experts=FAKE + 4), 6), (dict(offsets=FAKE + 4), 6), (dict(positions=FAKE + 2), 6), (dict(source=FAKE + 1), 6),
     (dict(ws=FAKE + 8), 6)])
 def test_sort_refusals(L, kw, status):
@@ -135,7 +135,7 @@ def test_lora_add_refusals(L, kw, status):
 
 
 @pytest.mark.parametrize("kw,status", [(dict(K=72, ldx=72), 2), (dict(flags=0x10), 3), (dict(c=None), 1), (dict(e=None), 1),
-                                       (dict(y=FAKE + 2), 6)])
+                                       (dict(y=FAKE + 2), 6), (dict(M=1 << 20, N=1 << 17), 2)])
 def test_nvfp4_lora_refusals(L, kw, status):
     assert call(L, "nvfp4_lora_matvec", MATVEC, kw) == status
 
@@ -144,6 +144,10 @@ def test_lora_workspace(L):
     assert L.lora_workspace_bytes(16, 16) >= 16 * 16 * 4
     for bad in ((-1, 16), ((1 << 20) + 1, 16), (4, 0), (4, 12), (4, 264)):
         assert L.lora_workspace_bytes(*bad) == -1
+        assert L.nvfp4_lora_workspace_bytes(bad[0], 64, bad[1], 0) == -1
+    assert L.nvfp4_lora_workspace_bytes(16, 100, 16, 0) >= L.lora_workspace_bytes(16, 16) + 6400
+    assert L.nvfp4_lora_workspace_bytes(16, 100, 16, 1) >= L.lora_workspace_bytes(16, 16)
+    assert L.nvfp4_lora_workspace_bytes(16, -1, 16, 0) == -1 and L.nvfp4_lora_workspace_bytes(16, 64, 16, 2) == -1
     assert call(L, "lora_add", ADD, dict(M=0, y=None, out=None, ws=None)) == 0
     assert call(L, "nvfp4_lora_matvec", MATVEC, dict(N=0, y=None, ws=None)) == 0
 
