@@ -54,17 +54,26 @@ __global__ __launch_bounds__(64 * lora_waves(NR)) void lora_down_kernel(LoraArgs
     uint8_t* mine = lds + wave * ROWS * LORA_PITCH;
     for_adapters(ids, blockIdx.y, gridDim.y, [&](int id) {
         const uint32_t rows = (uint32_t)__ballot(ids == id) & 0xFFFFu;   // the tile's tokens with this adapter
-        // a lane's rows: tokens row8 and 8 + row8, ranks rank0 + 8 i + row8; the others count as zeros
-        const uint16_t* x = a.x + (m0 + row8) * a.ldx + k8;
-        const uint16_t* w = a.a + ((int64_t)id * a.r + rank0 + row8) * a.K + k8;
+        // a lane's rows: tokens row8 and 8 + row8, ranks rank0 + 8 i + row8.  In the place of a token with another
+        // adapter and of a rank past r, whose results nobody takes, one that is there stands.
+        const uint16_t* from[2 * (NR + 1)];
+#pragma unroll
+        for (int i = 0; i < 2 * (NR + 1); ++i) {
+            const int token = 8 * i + row8, rank = rank0 + 8 * (i - 2) + row8;
+            from[i] = k8 + (i < 2 ? a.x + (m0 + ((rows >> token) & 1 ? token : __builtin_ctz(rows))) * a.ldx
+                                  : a.a + ((int64_t)id * a.r + (rank < a.r ? rank : a.r - 1)) * a.K);
+        }
         uint4 v[D][2 * (NR + 1)];
         auto load = [&](int d, int c) {
-            const bool in = 64 * c + k8 < K;
+            if (64 * (c + 1) <= K) {
 #pragma unroll
-            for (int i = 0; i < 2 * (NR + 1); ++i) {
-                v[d][i] = make_uint4(0, 0, 0, 0);
-                const bool on = i < 2 ? (rows >> (8 * i + row8)) & 1 : rank0 + 8 * (i - 2) + row8 < a.r;
-                if (on && in) v[d][i] = *(const uint4*)((i < 2 ? x + 8 * i * a.ldx : w + 8 * (i - 2) * a.K) + 64 * c);
+                for (int i = 0; i < 2 * (NR + 1); ++i) v[d][i] = *(const uint4*)(from[i] + 64 * c);
+            } else {   // the piece that K ends in
+#pragma unroll
+                for (int i = 0; i < 2 * (NR + 1); ++i) {
+                    v[d][i] = make_uint4(0, 0, 0, 0);
+                    if (64 * c + k8 < K) v[d][i] = *(const uint4*)(from[i] + 64 * c);
+                }
             }
         };
         floatx4 acc[NR];

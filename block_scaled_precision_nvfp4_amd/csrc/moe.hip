@@ -268,6 +268,20 @@ struct MoeSlots {
     }
 };
 
+// Stores of 16 bytes; with NT past the caches, for outputs that they could not hold until somebody reads them: half of
+// the memory-side cache or more, in rows of whole 128-byte lines (a line that two rows share would be written twice:
+// 45 us instead of 34 for MXFP8 rows of 2080 bytes).  us with and without, 402 and 670 MB moved: combination 60.9 and
+// 62.5, its backward 100 and 122, gather 69 and 75.
+template <bool NT>
+__device__ __forceinline__ void put(void* p, const uint4 v) {
+    if constexpr (NT) __builtin_nontemporal_store(u32v4{v.x, v.y, v.z, v.w}, (u32v4*)p);
+    else *(uint4*)p = v;
+}
+
+static bool past_caches(int64_t rows, int64_t row_bytes) {
+    return row_bytes % 128 == 0 && rows * row_bytes >= (int64_t)128 << 20;
+}
+
 struct GatherArgs {
     const uint16_t* x;
     int64_t ldx, H;
@@ -279,14 +293,14 @@ struct GatherArgs {
 };
 
 // A token's row is read once and written k times.  A wave takes 512 U elements of a token.
-template <int U>
+template <int U, bool NT>
 __global__ __launch_bounds__(MOE_THREADS) void moe_gather_kernel(GatherArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     uint16_t* out = (uint16_t*)a.out;
     if (blockIdx.x >= a.token_groups) {
         const int64_t w = (int64_t)(blockIdx.x - a.token_groups) * MOE_WAVES + wave;
         for_empty_rows(a.s.source, a.s.rows, a.s.T * a.s.k, w, (int64_t)(gridDim.x - a.token_groups) * MOE_WAVES, [&](int64_t r) {
-            for (int64_t c = 8 * lane; c < a.H; c += 512) *(uint4*)(out + r * a.H + c) = make_uint4(0, 0, 0, 0);
+            for (int64_t c = 8 * lane; c < a.H; c += 512) put<NT>(out + r * a.H + c, make_uint4(0, 0, 0, 0));
         });
         return;
     }
@@ -302,7 +316,7 @@ __global__ __launch_bounds__(MOE_THREADS) void moe_gather_kernel(GatherArgs a) {
         if (r < 0) continue;
 #pragma unroll
         for (int i = 0; i < U; ++i)
-            if (c0 + 512 * i < a.H) *(uint4*)(out + r * a.H + c0 + 512 * i) = v[i];
+            if (c0 + 512 * i < a.H) put<NT>(out + r * a.H + c0 + 512 * i, v[i]);
     }
 }
 
@@ -311,19 +325,19 @@ static unsigned empty_groups(int64_t rows) {   // a wave for 64 rows, at most 10
     return (unsigned)(g < 1 ? 1 : g > 1024 ? 1024 : g);
 }
 
-template <int U>
-static int launch_gather(GatherArgs a, hipStream_t s) {
-    const int64_t waves = a.s.T * ((a.H + 512 * U - 1) / (512 * U));
-    a.token_groups = (unsigned)((waves + MOE_WAVES - 1) / MOE_WAVES);
-    hipLaunchKernelGGL((moe_gather_kernel<U>), dim3(a.token_groups + empty_groups(a.s.rows)), dim3(MOE_THREADS), 0, s, a);
-    return (int)hipGetLastError();
+constexpr int GATHER_U = 4;   // vectors of a lane: 2 and 8 within 2 %
+static unsigned gather_groups(int64_t T, int64_t H) {
+    return (unsigned)((T * ((H + 512 * GATHER_U - 1) / (512 * GATHER_U)) + MOE_WAVES - 1) / MOE_WAVES);
 }
 
 int launch_moe_gather(const void* x, int64_t ldx, int64_t T, int64_t k, int64_t H, const int32_t* positions,
                       const int32_t* source, int64_t rows, void* out, void* hip_stream) {
     if (rows == 0 || H == 0) return 0;
-    return launch_gather<4>({(const uint16_t*)x, ldx, H, {positions, source, T, (int)k, rows}, 0, out, nullptr, nullptr},
-                            (hipStream_t)hip_stream);
+    const GatherArgs a{(const uint16_t*)x, ldx, H, {positions, source, T, (int)k, rows}, gather_groups(T, H), out, nullptr, nullptr};
+    const dim3 grid(a.token_groups + empty_groups(rows)), block(MOE_THREADS);
+    if (past_caches(rows, H * 2)) hipLaunchKernelGGL((moe_gather_kernel<GATHER_U, true>), grid, block, 0, (hipStream_t)hip_stream, a);
+    else hipLaunchKernelGGL((moe_gather_kernel<GATHER_U, false>), grid, block, 0, (hipStream_t)hip_stream, a);
+    return (int)hipGetLastError();
 }
 
 __device__ __forceinline__ float max8(const float v[8]) {
@@ -397,10 +411,8 @@ __global__ __launch_bounds__(MOE_THREADS) void moe_gather_mxfp8_kernel(GatherArg
 int launch_moe_gather_mxfp8(const void* x, int64_t ldx, int64_t T, int64_t k, int64_t H, const int32_t* positions,
                             const int32_t* source, int64_t rows, uint8_t* codes, uint8_t* scales, void* hip_stream) {
     if (rows == 0 || H == 0) return 0;
-    GatherArgs a{(const uint16_t*)x, ldx, H, {positions, source, T, (int)k, rows}, 0, codes, scales, nullptr};
-    const int64_t waves = T * ((H + 2047) / 2048);
-    a.token_groups = (unsigned)((waves + MOE_WAVES - 1) / MOE_WAVES);
-    hipLaunchKernelGGL((moe_gather_mxfp8_kernel<4>), dim3(a.token_groups + empty_groups(rows)), dim3(MOE_THREADS), 0,
+    const GatherArgs a{(const uint16_t*)x, ldx, H, {positions, source, T, (int)k, rows}, gather_groups(T, H), codes, scales, nullptr};
+    hipLaunchKernelGGL((moe_gather_mxfp8_kernel<GATHER_U>), dim3(a.token_groups + empty_groups(rows)), dim3(MOE_THREADS), 0,
                        (hipStream_t)hip_stream, a);
     return (int)hipGetLastError();
 }
@@ -511,14 +523,14 @@ struct Row8 {
     }
 };
 
-template <bool F32>
+template <bool F32, bool NT>
 __device__ __forceinline__ void store8(void* y, int64_t at, const float v[8]) {
     if constexpr (F32) {
-        *(float4*)((float*)y + at) = make_float4(v[0], v[1], v[2], v[3]);
-        *(float4*)((float*)y + at + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        put<NT>((float*)y + at, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+        put<NT>((float*)y + at + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
     } else {
-        *(uint4*)((uint16_t*)y + at) =
-            make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
+        put<NT>((uint16_t*)y + at,
+                make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])));
     }
 }
 
@@ -531,7 +543,7 @@ struct CombineArgs {
 };
 
 // Sums in fp32 over j in ascending order, one rounding to the output's type.
-template <bool YF32, bool OF32>
+template <bool YF32, bool OF32, bool NT>
 __global__ __launch_bounds__(MOE_THREADS) void moe_combine_kernel(CombineArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int64_t pieces = (a.H + 511) / 512;
@@ -549,7 +561,7 @@ __global__ __launch_bounds__(MOE_THREADS) void moe_combine_kernel(CombineArgs a)
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(w, v[e], acc[e]);
     }
-    store8<OF32>(a.out, t * a.H + c, acc);
+    store8<OF32, NT>(a.out, t * a.H + c, acc);
 }
 
 int launch_moe_combine(const void* y, int y_f32, int64_t T, int64_t k, int64_t H, const int32_t* positions, int64_t rows,
@@ -558,10 +570,15 @@ int launch_moe_combine(const void* y, int y_f32, int64_t T, int64_t k, int64_t H
     hipStream_t s = (hipStream_t)hip_stream;
     const CombineArgs a{y, H, {positions, nullptr, T, (int)k, rows}, weights, out};
     const dim3 grid((unsigned)((T * ((H + 511) / 512) + MOE_WAVES - 1) / MOE_WAVES)), block(MOE_THREADS);
-    if (y_f32 && out_f32) hipLaunchKernelGGL((moe_combine_kernel<true, true>), grid, block, 0, s, a);
-    else if (y_f32) hipLaunchKernelGGL((moe_combine_kernel<true, false>), grid, block, 0, s, a);
-    else if (out_f32) hipLaunchKernelGGL((moe_combine_kernel<false, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((moe_combine_kernel<false, false>), grid, block, 0, s, a);
+    auto launch = [&](auto nt_c) {
+        constexpr bool NT = decltype(nt_c)::value;
+        if (y_f32 && out_f32) hipLaunchKernelGGL((moe_combine_kernel<true, true, NT>), grid, block, 0, s, a);
+        else if (y_f32) hipLaunchKernelGGL((moe_combine_kernel<true, false, NT>), grid, block, 0, s, a);
+        else if (out_f32) hipLaunchKernelGGL((moe_combine_kernel<false, true, NT>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((moe_combine_kernel<false, false, NT>), grid, block, 0, s, a);
+    };
+    if (past_caches(T, H * (out_f32 ? 4 : 2))) launch(std::true_type{});
+    else launch(std::false_type{});
     return (int)hipGetLastError();
 }
 
@@ -578,14 +595,14 @@ struct CombineBwdArgs {
 
 // A wave takes a slot: the token's row of dout (which the waves of its other slots read about the same time, so that it
 // comes from memory once) with the slot's row of y, U pieces of 512 elements at a time.
-template <bool YF32, int U>
+template <bool YF32, int U, bool NT>
 __global__ __launch_bounds__(MOE_THREADS) void moe_combine_backward_kernel(CombineBwdArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     if (blockIdx.x >= a.token_groups) {
         const int64_t w = (int64_t)(blockIdx.x - a.token_groups) * MOE_WAVES + wave;
         for_empty_rows(a.s.source, a.s.rows, a.s.T * a.s.k, w, (int64_t)(gridDim.x - a.token_groups) * MOE_WAVES, [&](int64_t r) {
             const float zero[8] = {};
-            for (int64_t c = 8 * lane; c < a.H; c += 512) store8<YF32>(a.dy, r * a.H + c, zero);
+            for (int64_t c = 8 * lane; c < a.H; c += 512) store8<YF32, NT>(a.dy, r * a.H + c, zero);
         });
         return;
     }
@@ -619,7 +636,7 @@ __global__ __launch_bounds__(MOE_THREADS) void moe_combine_backward_kernel(Combi
                     dot = __builtin_fmaf(x[e], v[e], dot);
                     x[e] = w * x[e];
                 }
-                store8<YF32>(a.dy, (int64_t)r * a.H + c0 + 512 * u, x);
+                store8<YF32, NT>(a.dy, (int64_t)r * a.H + c0 + 512 * u, x);
             }
     }
 #pragma unroll
@@ -635,8 +652,13 @@ int launch_moe_combine_backward(const void* dout, const void* y, int y_f32, int6
     const unsigned tg = (unsigned)((T * k + MOE_WAVES - 1) / MOE_WAVES);
     const CombineBwdArgs a{(const uint16_t*)dout, y, H, {positions, source, T, (int)k, rows}, weights, dy, dweights, tg};
     const dim3 grid(tg + empty_groups(rows)), block(MOE_THREADS);
-    if (y_f32) hipLaunchKernelGGL((moe_combine_backward_kernel<true, 2>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((moe_combine_backward_kernel<false, 4>), grid, block, 0, s, a);
+    auto launch = [&](auto nt_c) {
+        constexpr bool NT = decltype(nt_c)::value;
+        if (y_f32) hipLaunchKernelGGL((moe_combine_backward_kernel<true, 2, NT>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((moe_combine_backward_kernel<false, 4, NT>), grid, block, 0, s, a);
+    };
+    if (past_caches(rows, H * (y_f32 ? 4 : 2))) launch(std::true_type{});
+    else launch(std::false_type{});
     return (int)hipGetLastError();
 }
 
