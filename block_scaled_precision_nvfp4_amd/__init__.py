@@ -830,7 +830,8 @@ def moe_combine(y: torch.Tensor, positions: torch.Tensor, weights: Optional[torc
     if y.dim() != 2:
         raise ValueError("y must be [rows, H]")
     dev, (R, H) = y.device, y.shape
-    _dev_tensor(positions, torch.int32, "positions")
+    if not isinstance(positions, torch.Tensor) or positions.dim() != 2:
+        raise ValueError("positions must be [tokens, k]")
     T = positions.shape[0]
     k = _slots(positions, T, dev)
     _slot_weights(weights, positions)

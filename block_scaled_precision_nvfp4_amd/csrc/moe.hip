@@ -261,12 +261,39 @@ struct MoeSlots {
     int64_t T;
     int k;
     int64_t rows;
-    // slot j's row of token t, -1: none
-    __device__ __forceinline__ int64_t row(int64_t t, int j) const {
-        const int32_t p = positions[t * k + j];
-        return p >= 0 && p < rows ? p : -1;
-    }
 };
+
+// The rows of token t's slots, k <= 64 of them: lane j fetches slot j's, all in one trip to memory.  Fetched one after
+// another (for_slots with FEW false), each waits for a trip of its own; a full chip does not mind, and MXFP8 rows, and
+// a combination of few, do better so paced.  us with lanes and one after another: 64 tokens x 8 of 4096, MXFP8 4.2
+// and 5.1, combination 4.3 and 6.6; MXFP8 8192 x 8 of 2048 35.8 and 29.0, combination 16384 x 2 of 4096 65.8 and 61.0.
+struct TokenRows {
+    int32_t p;
+    uint64_t left;   // slots that have a row, in ascending order
+    __device__ __forceinline__ TokenRows(const MoeSlots& s, int64_t t) {
+        const int lane = threadIdx.x & 63;
+        p = lane < s.k ? s.positions[t * s.k + lane] : -1;
+        left = __ballot(p >= 0 && p < s.rows);
+    }
+    __device__ __forceinline__ int slot() const { return __builtin_ctzll(left); }
+    __device__ __forceinline__ int64_t row() const { return __builtin_amdgcn_readlane(p, slot()); }
+    __device__ __forceinline__ void next() { left &= left - 1; }
+};
+
+static bool few_tokens(int64_t waves) { return waves < 2048; }   // eight for each CU
+
+// Calls body(slot, row) for token t's slots that have a row, in ascending order.
+template <bool FEW, class F>
+__device__ __forceinline__ void for_slots(const MoeSlots& s, int64_t t, F&& body) {
+    if constexpr (FEW) {
+        for (TokenRows rows(s, t); rows.left; rows.next()) body(rows.slot(), rows.row());
+    } else {
+        for (int j = 0; j < s.k; ++j) {
+            const int32_t r = s.positions[t * s.k + j];
+            if (r >= 0 && r < s.rows) body(j, (int64_t)r);
+        }
+    }
+}
 
 // Stores of 16 bytes; with NT past the caches, for outputs that they could not hold until somebody reads them: half of
 // the memory-side cache or more, in rows of whole 128-byte lines (a line that two rows share would be written twice:
@@ -307,13 +334,13 @@ __global__ __launch_bounds__(MOE_THREADS) void moe_gather_kernel(GatherArgs a) {
     const int64_t pieces = (a.H + 512 * U - 1) / (512 * U);
     const int64_t u = (int64_t)blockIdx.x * MOE_WAVES + wave, t = u / pieces, c0 = (u % pieces) * (512 * U) + 8 * lane;
     if (t >= a.s.T) return;
+    TokenRows rows(a.s, t);
     uint4 v[U];
 #pragma unroll
     for (int i = 0; i < U; ++i)
         if (c0 + 512 * i < a.H) v[i] = load16_stream(a.x + t * a.ldx + c0 + 512 * i);
-    for (int j = 0; j < a.s.k; ++j) {
-        const int64_t r = a.s.row(t, j);
-        if (r < 0) continue;
+    for (; rows.left; rows.next()) {
+        const int64_t r = rows.row();
 #pragma unroll
         for (int i = 0; i < U; ++i)
             if (c0 + 512 * i < a.H) put<NT>(out + r * a.H + c0 + 512 * i, v[i]);
@@ -367,7 +394,7 @@ __device__ __forceinline__ void mx_row_unit(const uint4 q, uint2& w, uint32_t& s
 }
 
 // MXFP8: a token is cast once, and its codes and scales written k times.  A lane holds a quarter of a block of 32.
-template <int U>
+template <int U, bool FEW>
 __global__ __launch_bounds__(MOE_THREADS) void moe_gather_mxfp8_kernel(GatherArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     uint8_t* codes = (uint8_t*)a.out;
@@ -395,9 +422,7 @@ __global__ __launch_bounds__(MOE_THREADS) void moe_gather_mxfp8_kernel(GatherArg
     for (int i = 0; i < U; ++i) {
         mx_row_unit(q[i], w[i], sb[i]);
     }
-    for (int j = 0; j < a.s.k; ++j) {
-        const int64_t r = a.s.row(t, j);
-        if (r < 0) continue;
+    for_slots<FEW>(a.s, t, [&](int, int64_t r) {
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int64_t c = c0 + 512 * i;
@@ -405,22 +430,24 @@ __global__ __launch_bounds__(MOE_THREADS) void moe_gather_mxfp8_kernel(GatherArg
             *(uint2*)(codes + r * a.H + c) = w[i];
             if ((lane & 3) == 0) a.scales[r * S + c / 32] = (uint8_t)sb[i];
         }
-    }
+    });
 }
 
 int launch_moe_gather_mxfp8(const void* x, int64_t ldx, int64_t T, int64_t k, int64_t H, const int32_t* positions,
                             const int32_t* source, int64_t rows, uint8_t* codes, uint8_t* scales, void* hip_stream) {
     if (rows == 0 || H == 0) return 0;
     const GatherArgs a{(const uint16_t*)x, ldx, H, {positions, source, T, (int)k, rows}, gather_groups(T, H), codes, scales, nullptr};
-    hipLaunchKernelGGL((moe_gather_mxfp8_kernel<GATHER_U>), dim3(a.token_groups + empty_groups(rows)), dim3(MOE_THREADS), 0,
-                       (hipStream_t)hip_stream, a);
+    const dim3 grid(a.token_groups + empty_groups(rows)), block(MOE_THREADS);
+    if (few_tokens((int64_t)a.token_groups * MOE_WAVES))
+        hipLaunchKernelGGL((moe_gather_mxfp8_kernel<GATHER_U, true>), grid, block, 0, (hipStream_t)hip_stream, a);
+    else
+        hipLaunchKernelGGL((moe_gather_mxfp8_kernel<GATHER_U, false>), grid, block, 0, (hipStream_t)hip_stream, a);
     return (int)hipGetLastError();
 }
 
-// Row-scaled NVFP4: a workgroup takes a token, whose largest magnitude comes first.  Up to NV_UNITS vectors a thread
-// stay in registers in between; longer rows are read twice.  A lane pair holds a block of 16.
-constexpr int NV_UNITS = 4;
-
+// Row-scaled NVFP4: W waves take a token, whose largest magnitude comes first; a lane holds whole blocks of 16.  U
+// blocks a lane stay in registers in between; longer rows (W = 4 only) are read twice.
+template <int U, int W>
 __global__ __launch_bounds__(MOE_THREADS) void moe_gather_nvfp4_kernel(GatherArgs a) {
     __shared__ float red[MOE_WAVES];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -429,59 +456,72 @@ __global__ __launch_bounds__(MOE_THREADS) void moe_gather_nvfp4_kernel(GatherArg
     if (blockIdx.x >= a.token_groups) {
         const int64_t w = (int64_t)(blockIdx.x - a.token_groups) * MOE_WAVES + wave;
         for_empty_rows(a.s.source, a.s.rows, a.s.T * a.s.k, w, (int64_t)(gridDim.x - a.token_groups) * MOE_WAVES, [&](int64_t r) {
-            for (int64_t c = 8 * lane; c < C; c += 512) *(uint2*)(codes + r * C + c) = make_uint2(0, 0);
-            for (int64_t b = lane; b < S; b += 64) a.scales[r * S + b] = 0;
+            for (int64_t b = lane; b < S; b += 64) {
+                *(uint2*)(codes + r * C + 8 * b) = make_uint2(0, 0);
+                a.scales[r * S + b] = 0;
+            }
             if (lane == 0) a.s_enc[r] = 1.0f;
         });
         return;
     }
-    const int64_t t = blockIdx.x;
+    const int64_t t = W == 1 ? (int64_t)blockIdx.x * MOE_WAVES + wave : (int64_t)blockIdx.x;
+    if (W == 1 && t >= a.s.T) return;
+    const TokenRows all(a.s, t);
+    const int first = W == 1 ? lane : (int)threadIdx.x;   // the thread's first block; its others 64 W apart
     const uint16_t* x = a.x + t * a.ldx;
-    const bool one = a.H <= 8 * NV_UNITS * MOE_THREADS;
-    uint4 q[NV_UNITS];
+    const bool one = W == 1 || S <= 64 * U * W;
+    uint4 q[U][2];
     float m = 0.0f;
-    auto load = [&](int64_t c0) {
+    auto load = [&](int64_t b0) {
 #pragma unroll
-        for (int i = 0; i < NV_UNITS; ++i) {
-            const int64_t c = c0 + 8 * ((int64_t)threadIdx.x + MOE_THREADS * i);
-            q[i] = make_uint4(0, 0, 0, 0);
-            if (c < a.H) q[i] = *(const uint4*)(x + c);
+        for (int i = 0; i < U; ++i) {
+            const int64_t b = b0 + first + 64 * W * i;
+            q[i][0] = q[i][1] = make_uint4(0, 0, 0, 0);
+            if (b < S) {
+                q[i][0] = *(const uint4*)(x + 16 * b);
+                q[i][1] = *(const uint4*)(x + 16 * b + 8);
+            }
         }
     };
-    for (int64_t c0 = 0; c0 < a.H; c0 += 8 * NV_UNITS * MOE_THREADS) {
-        load(c0);
+    auto values = [&](int i, float v[16]) {
+        unpack_bf16x8(q[i][0], v);
+        unpack_bf16x8(q[i][1], v + 8);
+        return __builtin_fmaxf(max8(v), max8(v + 8));
+    };
+    for (int64_t b0 = 0; b0 < S; b0 += 64 * U * W) {
+        load(b0);
 #pragma unroll
-        for (int i = 0; i < NV_UNITS; ++i) {
-            float v[8];
-            unpack_bf16x8(q[i], v);
-            m = __builtin_fmaxf(m, max8(v));
+        for (int i = 0; i < U; ++i) {
+            float v[16];
+            m = __builtin_fmaxf(m, values(i, v));
         }
     }
     m = wave_max(m);
-    if (lane == 0) red[wave] = m;
-    __syncthreads();
+    if constexpr (W > 1) {
+        if (lane == 0) red[wave] = m;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < MOE_WAVES; ++w) m = __builtin_fmaxf(m, red[w]);
+        for (int w = 0; w < W; ++w) m = __builtin_fmaxf(m, red[w]);
+    }
     const float Se = nvfp4_tensor_scale(m);
-    for (int64_t c0 = 0; c0 < a.H; c0 += 8 * NV_UNITS * MOE_THREADS) {
-        if (!one) load(c0);
-        uint32_t w[NV_UNITS], sb[NV_UNITS];
+    for (int64_t b0 = 0; b0 < S; b0 += 64 * U * W) {
+        if (!one) load(b0);
+        uint32_t w[U][2], sb[U];
 #pragma unroll
-        for (int i = 0; i < NV_UNITS; ++i) {
-            float v[8];
-            unpack_bf16x8(q[i], v);
-            sb[i] = encode_block<8, false, false>(v, pair_max(max8(v)), Se, nullptr, 0, 0, 0, 0, &w[i]);
+        for (int i = 0; i < U; ++i) {
+            float v[16];
+            const float bm = values(i, v);
+            sb[i] = encode_block<16, false, false>(v, bm, Se, nullptr, 0, 0, 0, 0, w[i]);
         }
-        for (int j = 0; j < a.s.k; ++j) {
-            const int64_t r = a.s.row(t, j);
-            if (r < 0) continue;
-            if (c0 == 0 && threadIdx.x == 0) a.s_enc[r] = Se;
+        for (TokenRows rows = all; rows.left; rows.next()) {
+            const int64_t r = rows.row();
+            if (b0 == 0 && first == 0) a.s_enc[r] = Se;
 #pragma unroll
-            for (int i = 0; i < NV_UNITS; ++i) {
-                const int64_t c = c0 + 8 * ((int64_t)threadIdx.x + MOE_THREADS * i);
-                if (c >= a.H) continue;
-                *(uint32_t*)(codes + r * C + c / 2) = w[i];
-                if ((lane & 1) == 0) a.scales[r * S + c / 16] = (uint8_t)sb[i];
+            for (int i = 0; i < U; ++i) {
+                const int64_t b = b0 + first + 64 * W * i;
+                if (b >= S) continue;
+                *(uint2*)(codes + r * C + 8 * b) = make_uint2(w[i][0], w[i][1]);
+                a.scales[r * S + b] = (uint8_t)sb[i];
             }
         }
     }
@@ -491,9 +531,16 @@ int launch_moe_gather_nvfp4(const void* x, int64_t ldx, int64_t T, int64_t k, in
                             const int32_t* source, int64_t rows, uint8_t* codes, uint8_t* scales, float* s_enc,
                             void* hip_stream) {
     if (rows == 0) return 0;
-    GatherArgs a{(const uint16_t*)x, ldx, H, {positions, source, T, (int)k, rows}, (unsigned)T, codes, scales, s_enc};
-    hipLaunchKernelGGL(moe_gather_nvfp4_kernel, dim3(a.token_groups + empty_groups(rows)), dim3(MOE_THREADS), 0,
-                       (hipStream_t)hip_stream, a);
+    hipStream_t s = (hipStream_t)hip_stream;
+    // a wave a token where that leaves every CU eight of them, else a workgroup
+    const bool wave = T >= 2048 && H <= 4096;
+    const GatherArgs a{(const uint16_t*)x, ldx, H, {positions, source, T, (int)k, rows},
+                       (unsigned)(wave ? (T + MOE_WAVES - 1) / MOE_WAVES : T), codes, scales, s_enc};
+    const dim3 grid(a.token_groups + empty_groups(rows)), block(MOE_THREADS);
+    if (wave && H <= 2048) hipLaunchKernelGGL((moe_gather_nvfp4_kernel<2, 1>), grid, block, 0, s, a);
+    else if (wave) hipLaunchKernelGGL((moe_gather_nvfp4_kernel<4, 1>), grid, block, 0, s, a);
+    else if (H <= 4096) hipLaunchKernelGGL((moe_gather_nvfp4_kernel<1, 4>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((moe_gather_nvfp4_kernel<2, 4>), grid, block, 0, s, a);
     return (int)hipGetLastError();
 }
 
@@ -543,23 +590,47 @@ struct CombineArgs {
 };
 
 // Sums in fp32 over j in ascending order, one rounding to the output's type.
-template <bool YF32, bool OF32, bool NT>
+template <bool YF32, bool OF32, bool NT, bool FEW>
 __global__ __launch_bounds__(MOE_THREADS) void moe_combine_kernel(CombineArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int64_t pieces = (a.H + 511) / 512;
     const int64_t u = (int64_t)blockIdx.x * MOE_WAVES + wave, t = u / pieces, c = (u % pieces) * 512 + 8 * lane;
-    if (t >= a.s.T || c >= a.H) return;
+    if (t >= a.s.T) return;
     float acc[8] = {};
-    for (int j = 0; j < a.s.k; ++j) {
-        const int64_t r = a.s.row(t, j);
-        if (r < 0) continue;
-        const float w = a.weights ? a.weights[t * a.s.k + j] : 1.0f;
-        Row8<YF32> q;
-        q.load(a.y, r * a.H + c);
-        float v[8];
-        q.values(v);
+    auto add = [&](float w, const Row8<YF32>& q) {
+        float y[8];
+        q.values(y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(w, v[e], acc[e]);
+        for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(w, y[e], acc[e]);
+    };
+    if constexpr (FEW) {
+        constexpr int G = 4;   // rows in flight
+        TokenRows rows(a.s, t);
+        const float weight = a.weights && lane < a.s.k ? a.weights[t * a.s.k + lane] : 1.0f;   // of slot `lane`
+        while (rows.left) {
+            float w[G];
+            Row8<YF32> q[G];
+            int n = 0;
+#pragma unroll
+            for (int u = 0; u < G; ++u)
+                if (rows.left) {
+                    w[u] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), rows.slot()));
+                    if (c < a.H) q[u].load(a.y, rows.row() * a.H + c);
+                    rows.next();
+                    ++n;
+                }
+#pragma unroll
+            for (int u = 0; u < G; ++u)
+                if (u < n) add(w[u], q[u]);
+        }
+        if (c >= a.H) return;
+    } else {
+        if (c >= a.H) return;
+        for_slots<false>(a.s, t, [&](int j, int64_t r) {
+            Row8<YF32> q;
+            q.load(a.y, r * a.H + c);
+            add(a.weights ? a.weights[t * a.s.k + j] : 1.0f, q);
+        });
     }
     store8<OF32, NT>(a.out, t * a.H + c, acc);
 }
@@ -569,16 +640,18 @@ int launch_moe_combine(const void* y, int y_f32, int64_t T, int64_t k, int64_t H
     if (T == 0 || H == 0) return 0;
     hipStream_t s = (hipStream_t)hip_stream;
     const CombineArgs a{y, H, {positions, nullptr, T, (int)k, rows}, weights, out};
-    const dim3 grid((unsigned)((T * ((H + 511) / 512) + MOE_WAVES - 1) / MOE_WAVES)), block(MOE_THREADS);
-    auto launch = [&](auto nt_c) {
-        constexpr bool NT = decltype(nt_c)::value;
-        if (y_f32 && out_f32) hipLaunchKernelGGL((moe_combine_kernel<true, true, NT>), grid, block, 0, s, a);
-        else if (y_f32) hipLaunchKernelGGL((moe_combine_kernel<true, false, NT>), grid, block, 0, s, a);
-        else if (out_f32) hipLaunchKernelGGL((moe_combine_kernel<false, true, NT>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((moe_combine_kernel<false, false, NT>), grid, block, 0, s, a);
+    const int64_t waves = T * ((H + 511) / 512);
+    const dim3 grid((unsigned)((waves + MOE_WAVES - 1) / MOE_WAVES)), block(MOE_THREADS);
+    auto launch = [&](auto nt_c, auto few_c) {
+        constexpr bool NT = decltype(nt_c)::value, FEW = decltype(few_c)::value;
+        if (y_f32 && out_f32) hipLaunchKernelGGL((moe_combine_kernel<true, true, NT, FEW>), grid, block, 0, s, a);
+        else if (y_f32) hipLaunchKernelGGL((moe_combine_kernel<true, false, NT, FEW>), grid, block, 0, s, a);
+        else if (out_f32) hipLaunchKernelGGL((moe_combine_kernel<false, true, NT, FEW>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((moe_combine_kernel<false, false, NT, FEW>), grid, block, 0, s, a);
     };
-    if (past_caches(T, H * (out_f32 ? 4 : 2))) launch(std::true_type{});
-    else launch(std::false_type{});
+    if (past_caches(T, H * (out_f32 ? 4 : 2))) launch(std::true_type{}, std::false_type{});
+    else if (few_tokens(waves)) launch(std::false_type{}, std::true_type{});
+    else launch(std::false_type{}, std::false_type{});
     return (int)hipGetLastError();
 }
 
