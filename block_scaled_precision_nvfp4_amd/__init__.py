@@ -700,6 +700,16 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
 
 # ---------------------------------------------------------------- tokens and their experts
 
+def _call(fn: str, dev, *args):
+    """The C entry point on dev's current stream, which may belong to another device than the current one."""
+    f = getattr(lib(), fn)
+    if dev.index == torch.cuda.current_device():
+        _check(fn, f(*args, _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, f(*args, _stream(dev)))
+
+
 _TYPES = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
 
 
@@ -764,8 +774,8 @@ def moe_sort(experts: torch.Tensor, num_experts: int, align: int = 1,
     offsets = torch.empty(max(num_experts, 0) + 1, dtype=torch.int64, device=dev)
     positions = torch.empty_like(experts, dtype=torch.int32)
     source = torch.empty(max(rows, 0), dtype=torch.int32, device=dev)
-    _check("moe_sort", L.moe_sort(experts.data_ptr(), experts.element_size(), n, num_experts, align, rows,
-                                  offsets.data_ptr(), positions.data_ptr(), source.data_ptr(), _ptr(ws), _stream(dev)))
+    _call("moe_sort", dev, experts.data_ptr(), experts.element_size(), n, num_experts, align, rows, offsets.data_ptr(),
+          positions.data_ptr(), source.data_ptr(), _ptr(ws))
     return {"offsets": offsets, "positions": positions, "source": source}
 
 
@@ -777,8 +787,7 @@ def moe_gather(x: torch.Tensor, positions: torch.Tensor, source: torch.Tensor,
     dev = x.device
     k, R = _slots(positions, T, dev), _source(source, dev)
     out = _output(out, (R, H), torch.bfloat16, dev)
-    _check("moe_gather", lib().moe_gather(T, k, H, x.data_ptr(), ldx, positions.data_ptr(), source.data_ptr(), R,
-                                          out.data_ptr(), _stream(dev)))
+    _call("moe_gather", dev, T, k, H, x.data_ptr(), ldx, positions.data_ptr(), source.data_ptr(), R, out.data_ptr())
     return out
 
 
@@ -791,9 +800,8 @@ def moe_gather_nvfp4_rowscaled(x: torch.Tensor, positions: torch.Tensor, source:
     u8 = dict(dtype=torch.uint8, device=dev)
     out = {"codes": torch.empty((R, H // 2), **u8), "scales": torch.empty((R, H // 16), **u8),
            "s_enc": torch.empty(R, dtype=torch.float32, device=dev)}
-    _check("moe_gather_nvfp4_rowscaled", lib().moe_gather_nvfp4_rowscaled(
-        T, k, H, x.data_ptr(), ldx, positions.data_ptr(), source.data_ptr(), R, out["codes"].data_ptr(),
-        out["scales"].data_ptr(), out["s_enc"].data_ptr(), _stream(dev)))
+    _call("moe_gather_nvfp4_rowscaled", dev, T, k, H, x.data_ptr(), ldx, positions.data_ptr(), source.data_ptr(), R,
+          out["codes"].data_ptr(), out["scales"].data_ptr(), out["s_enc"].data_ptr())
     return out
 
 
@@ -805,9 +813,8 @@ def moe_gather_mxfp8(x: torch.Tensor, positions: torch.Tensor, source: torch.Ten
     k, R = _slots(positions, T, dev), _source(source, dev)
     u8 = dict(dtype=torch.uint8, device=dev)
     out = {"row_codes": torch.empty((R, H), **u8), "row_scales": torch.empty((R, H // 32), **u8)}
-    _check("moe_gather_mxfp8", lib().moe_gather_mxfp8(
-        T, k, H, x.data_ptr(), ldx, positions.data_ptr(), source.data_ptr(), R, out["row_codes"].data_ptr(),
-        out["row_scales"].data_ptr(), _stream(dev)))
+    _call("moe_gather_mxfp8", dev, T, k, H, x.data_ptr(), ldx, positions.data_ptr(), source.data_ptr(), R,
+          out["row_codes"].data_ptr(), out["row_scales"].data_ptr())
     return out
 
 
@@ -837,8 +844,7 @@ def moe_combine(y: torch.Tensor, positions: torch.Tensor, weights: Optional[torc
     _slot_weights(weights, positions)
     ot = _type(out_dtype, "out_dtype")
     out = _output(out, (T, H), out_dtype, dev)
-    _check("moe_combine", lib().moe_combine(T, k, H, y.data_ptr(), yt, R, positions.data_ptr(), _ptr(weights),
-                                            out.data_ptr(), ot, _stream(dev)))
+    _call("moe_combine", dev, T, k, H, y.data_ptr(), yt, R, positions.data_ptr(), _ptr(weights), out.data_ptr(), ot)
     return out
 
 
@@ -863,9 +869,8 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, positions: torch.T
         raise TypeError("weights must be a tensor")
     dy = torch.empty_like(y)
     dw = torch.empty_like(weights)
-    _check("moe_combine_backward", lib().moe_combine_backward(
-        T, k, H, dout.data_ptr(), y.data_ptr(), yt, R, positions.data_ptr(), source.data_ptr(), weights.data_ptr(),
-        dy.data_ptr(), dw.data_ptr(), _stream(dev)))
+    _call("moe_combine_backward", dev, T, k, H, dout.data_ptr(), y.data_ptr(), yt, R, positions.data_ptr(),
+          source.data_ptr(), weights.data_ptr(), dy.data_ptr(), dw.data_ptr())
     return dy, dw
 
 
@@ -916,9 +921,8 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, adapters: torch.Tensor, lora_a: t
         if (Mo, No) != (M, N) or out.device != dev:
             raise ValueError("out must be %s on %s" % ((M, N), dev))
     ws = _workspace(workspace, max(lib().lora_workspace_bytes(M, r), 0), dev)
-    _check("lora_add", lib().lora_add(M, N, K, r, n, x.data_ptr(), ldx, adapters.data_ptr(), lora_a.data_ptr(),
-                                      lora_b.data_ptr(), _ptr(scales), y.data_ptr(), ldy, out.data_ptr(), ldo, yt,
-                                      ws.data_ptr(), _stream(dev)))
+    _call("lora_add", dev, M, N, K, r, n, x.data_ptr(), ldx, adapters.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(),
+          _ptr(scales), y.data_ptr(), ldy, out.data_ptr(), ldo, yt, ws.data_ptr())
     return out
 
 
@@ -936,8 +940,7 @@ def nvfp4_lora_matvec(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
     y_dtype = _type(out_dtype, "out_dtype")
     out = _output(out, (M, N), out_dtype, dev)
     ws = _workspace(workspace, max(lib().nvfp4_lora_workspace_bytes(M, N, r, y_dtype), 0), dev)
-    _check("nvfp4_lora_matvec", lib().nvfp4_lora_matvec(
-        FMT_B_ROWSCALED if rows else 0, M, N, K, x.data_ptr(), ldx, w_codes.data_ptr(), w_scales.data_ptr(),
-        w_s_enc.data_ptr(), r, n, adapters.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(), _ptr(scales), out.data_ptr(),
-        y_dtype, ws.data_ptr(), _stream(dev)))
+    _call("nvfp4_lora_matvec", dev, FMT_B_ROWSCALED if rows else 0, M, N, K, x.data_ptr(), ldx, w_codes.data_ptr(),
+          w_scales.data_ptr(), w_s_enc.data_ptr(), r, n, adapters.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(),
+          _ptr(scales), out.data_ptr(), y_dtype, ws.data_ptr())
     return out

@@ -1,10 +1,17 @@
 // lora.hip -- low-rank adapters beside a projection, each token with its own: out[m] = y[m] + s_a (x[m] A_a^T) B_a^T with a
 // the token's adapter, A [L][r][K], B [L][N][r].
 //
-// Two kernels: the down products t[m] = x[m] A_a^T into the caller's workspace (fp32), then the up products
-// onto y, or beside NVFP4 weights inside the epilogue of their product (matvec.hip).  Tokens go in tiles of
-// 16, the rows of a matrix instruction; a tile's adapters are taken one after another, each over all 16 rows,
-// and a row keeps the result of its own.  Rows do not mix, so a NaN stays with its token, or its adapter's tokens.
+// Two kernels: the down products t[m] = x[m] A_a^T into the caller's workspace, then the up products onto y.
+// Few tokens are taken one by one, whatever their adapters; beside NVFP4 weights, their down products go along with
+// the weights' product (matvec.hip).  Many go in tiles of 16, the rows of a matrix instruction; a tile's adapters are
+// taken one after another, each over all 16 rows, and a row keeps the result of its own.  Rows do not mix, so a
+// NaN stays with its token, or its adapter's tokens.
+//
+// Bound by memory where tokens are many (x once, y once each way), by latency where they are few.  us in a graph, states
+// rotating through 800 MB: 16 tokens of 16 adapters, rank 16, 4096 x 4096 6.5; 64 of one adapter, rank 64, 12.7;
+// 1024 in runs, rank 16, 14336 x 4096 28; 4096 in runs of 8 adapters, rank 64, 4096 x 4096 40 (down 17, up 23; its
+// bytes alone take 23 at the rate of a large copy), tokens of the same 8 adapters shuffled 153: every tile then has
+// most of them.
 #include "launch.hpp"
 #include "lora.hpp"
 
@@ -35,9 +42,16 @@ __device__ __forceinline__ void for_adapters(int ids, int first, int step, F&& b
 // t of a tile: blockIdx.x tile, .y which of its adapters, .z 16 NR ranks.  The waves share K, 64 elements (a
 // 128-byte line) of every row at a time.  A wave reads whole lines, 8 lanes each, and turns them to the matrix
 // instruction's order through LDS of its own: read in that order, neighbouring lanes would touch 16 lines, 16 bytes
-// of each, at a quarter of the rate.  D pieces are in flight in registers.  The waves' sums are joined in LDS.
+// of each, at a quarter of the rate (25 us instead of 17).  D pieces are in flight in registers.  The waves' sums are
+// joined in LDS, and go out as the up products' fragments.
 constexpr int LORA_PITCH = 144;   // bytes between rows in LDS: the fragments' reads cover all banks
 constexpr int lora_waves(int nr) { return nr == 4 ? 8 : 16; }
+
+// Orders a wave's own accesses to LDS, which the hardware runs as they come, for the compiler.
+__device__ __forceinline__ void lora_wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
 
 template <int NR>
 __global__ __launch_bounds__(64 * lora_waves(NR)) void lora_down_kernel(LoraArgs a) {
@@ -82,7 +96,7 @@ __global__ __launch_bounds__(64 * lora_waves(NR)) void lora_down_kernel(LoraArgs
         auto use = [&](int d) {
 #pragma unroll
             for (int i = 0; i < 2 * (NR + 1); ++i) *(uint4*)(mine + (8 * i + row8) * LORA_PITCH + 2 * k8) = v[d][i];
-            __builtin_amdgcn_wave_barrier();   // a wave's LDS accesses run in order
+            lora_wave_fence();
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint8_t* f = mine + r16 * LORA_PITCH + 32 * g + 16 * h;
@@ -92,7 +106,7 @@ __global__ __launch_bounds__(64 * lora_waves(NR)) void lora_down_kernel(LoraArgs
                     acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, *(const bf16x8_t*)(f + 16 * (n + 1) * LORA_PITCH),
                                                                      acc[n], 0, 0, 0);
             }
-            __builtin_amdgcn_wave_barrier();
+            lora_wave_fence();
         };
         const int count = pieces > wave ? (pieces - wave - 1) / W + 1 : 0;   // pieces wave, wave + W, ...
 #pragma unroll

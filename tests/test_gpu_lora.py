@@ -259,3 +259,75 @@ def test_tokens_are_used_once_each_in_matching_ways():
     got = bsq.lora_add(y, x, ad, a, b, s, out=torch.empty_like(y))
     perm = torch.randperm(M, generator=torch.Generator().manual_seed(1)).to(DEV)
     assert torch.equal(bsq.lora_add(y[perm].contiguous(), x[perm].contiguous(), ad[perm].contiguous(), a, b, s), got[perm])
+
+
+# above 64 tokens: every number of 32-rank steps, ranks that end inside one, columns that end inside 64 and inside 4, tiles
+# of tokens that end inside one, and enough of them that a workgroup takes several columns and its adapters in turn
+MANY = [(65, 70, 72, 8, 2, True), (66, 64, 64, 24, 66, False), (80, 200, 136, 32, 3, False), (129, 131, 200, 40, 5, True),
+        (200, 68, 264, 72, 4, False), (100, 256, 128, 200, 3, False), (257, 320, 512, 256, 9, True), (1100, 72, 4104, 16, 3, True),
+        (4200, 1000, 72, 16, 9, True), (4200, 260, 64, 128, 3, False), (2100, 2052, 64, 256, 4, True)]
+
+
+@pytest.mark.parametrize("M,N,K,r,L,runs", MANY)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_add_to_many_tokens(M, N, K, r, L, runs, dtype):
+    note("lora add %d %d %d %d %d runs=%s %s" % (M, N, K, r, L, runs, dtype))
+    x, ad, a, b, s = case(M, N, K, r, L, seed=M + r, runs=runs)
+    y = gauss(M, N, seed=9, dtype=dtype)
+    v, e = lora64(x, ad, a, b, s)
+    want = y.cpu().double() + v
+    (o,), intact = guarded([(M, N)], dtype)
+    got = bsq.lora_add(y, x, ad, a, b, s, out=o)
+    intact()
+    assert_within(got, want, e + want.abs() * F32 + store_error(want, dtype), "out")
+    none = ((ad < 0) | (ad >= L)).cpu()
+    assert torch.equal(got.cpu()[none], y.cpu()[none])
+    o.copy_(y)
+    bsq.lora_add(o, x, ad, a, b, s)
+    intact()
+    assert torch.equal(o, got)
+
+
+@pytest.mark.parametrize("M,N,K,r,L", [(65, 130, 80, 24, 3), (300, 1033, 272, 64, 5), (1500, 96, 4112, 136, 2)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_matvec_of_many_tokens(M, N, K, r, L, dtype):
+    note("nvfp4 lora matvec %d %d %d %d %d %s" % (M, N, K, r, L, dtype))
+    x, ad, a, b, s = case(M, N, K, r, L, seed=M)
+    w = weights(N, K, 4)
+    base, S = product(x.cpu().double(), nvfp4_values(*w))
+    v, e = lora64(x, ad, a, b, s)
+    (o,), intact = guarded([(M, N)], dtype)
+    got = bsq.nvfp4_lora_matvec(x, *w, ad, a, b, s, out_dtype=dtype, out=o)
+    intact()
+    want = base + v
+    assert_within(got, want, sum_error(K, S) + e + want.abs() * F32 + store_error(want, dtype), "y")
+
+
+@pytest.mark.parametrize("M", [20, 300])
+def test_what_lies_in_the_workspace_does_not_matter(M):
+    N, K, r, L = 100, 200, 24, 5
+    x, ad, a, b, s = case(M, N, K - K % 16, r, L)
+    y, w = gauss(M, N, seed=8), weights(N, K - K % 16, 4)
+    n = max(bsq.lib().nvfp4_lora_workspace_bytes(M, N, r, bsq.OUT_BF16), bsq.lib().lora_workspace_bytes(M, r))
+    outs = []
+    for fill in (0, 255, 127):   # zeros, NaN, large values
+        ws = torch.full((n,), fill, dtype=torch.uint8, device=DEV)
+        outs.append((bsq.lora_add(y, x, ad, a, b, s, out=torch.empty_like(y), workspace=ws),
+                     bsq.nvfp4_lora_matvec(x, *w, ad, a, b, s, workspace=ws)))
+    for o in outs[1:]:
+        assert torch.equal(o[0], outs[0][0]) and torch.equal(o[1], outs[0][1])
+
+
+@pytest.mark.parametrize("M", [3, 100])
+def test_no_token_with_an_adapter(M):
+    N, K, r = 132, 64, 16
+    x, _, a, b, s = case(M, N, K, r, 2)
+    ad = torch.full((M,), -1, dtype=torch.int32, device=DEV)
+    for dtype in (torch.bfloat16, torch.float32):
+        y = gauss(M, N, seed=8, dtype=dtype)
+        y[0, 0], y[1, 1] = float("nan"), float("inf")
+        before = y.clone()
+        got = bsq.lora_add(y, x, ad, a, b, s, out=torch.zeros_like(y))
+        assert torch.equal(got.view(torch.uint8), before.view(torch.uint8))
+        bsq.lora_add(y, x, ad, a, b, s)
+        assert torch.equal(y.view(torch.uint8), before.view(torch.uint8))

@@ -408,3 +408,75 @@ def test_rows_past_two_to_the_31_elements():
     sl = s[live].long()
     want = (x[sl // k].float() * w.reshape(-1)[sl].unsqueeze(1)).to(torch.bfloat16)
     assert torch.equal(dy[live], want) and (dy[pick[src < 0]] == 0).all()
+
+
+# over 1024 slots a wave: counted twice instead of kept; with 16 waves a workgroup and with 8
+@pytest.mark.parametrize("T,k,E", [(1200007, 2, 8), (400003, 3, 700)])
+def test_sort_of_many_slots(T, k, E):
+    check_sort(ids(T, k, E, 3, drop=0.05), E, 64)
+
+
+# outputs of 128 MiB and more, in rows of whole lines and of others, go past the caches
+@pytest.mark.parametrize("H", [2048, 2056])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_large_outputs(H, dtype):
+    T, k, E = 33000, 2, 8
+    g = torch.Generator(device=DEV).manual_seed(1)
+    e = torch.rand((T, E), device=DEV, generator=g).topk(k, 1).indices
+    e[torch.rand((T, k), device=DEV, generator=g) < 0.02] = -1
+    o = bsq.moe_sort(e, E, 32)
+    p, s = o["positions"], o["source"]
+    x = torch.randn((T, H), device=DEV, generator=g).to(torch.bfloat16)
+    w = torch.rand((T, k), device=DEV, generator=g)
+    src = s.long()
+    none = (src < 0).unsqueeze(1)
+    xs = bsq.moe_gather(x, p, s)
+    assert torch.equal(xs, torch.where(none, 0, x[src.clamp(min=0) // k]))
+    y = xs.to(dtype)
+    live = (p >= 0).unsqueeze(2)
+    rows = torch.where(live, y[p.clamp(min=0).reshape(-1).long()].reshape(T, k, H).double(), 0)
+    want, S = (rows * w.unsqueeze(2)).sum(1), (rows.abs() * w.unsqueeze(2)).sum(1)
+    for od in (torch.bfloat16, torch.float32):
+        got = bsq.moe_combine(y, p, w, out_dtype=od).double()
+        step = 2.0 ** -8 if od == torch.bfloat16 else F32
+        assert ((got - want).abs() <= k * F32 * S + want.abs() * step + 2.0 ** -134).all()
+    dy, dw = bsq.moe_combine_backward(x, y, p, s, w)
+    prod = x.float()[src.clamp(min=0) // k] * w.reshape(-1)[src.clamp(min=0)].unsqueeze(1)   # one rounding to fp32
+    assert torch.equal(dy, torch.where(none, 0, prod).to(dtype))
+    dots = rows * x.double().unsqueeze(1)
+    assert ((dw.double() - dots.sum(2)).abs() <= (H + 1) * F32 * dots.abs().sum(2)).all()
+
+
+def test_few_and_many_tokens_agree():
+    """The kernels fetch a token's slots in another way where tokens are few: the same bits either way."""
+    T, k, E, H = 3000, 5, 12, 512
+    p, s = order_of(T, k, E, 32, 21)
+    y, w = gauss(s.numel(), H, seed=1).to(DEV), torch.rand((T, k), device=DEV)
+    many = bsq.moe_combine(y, p, w)
+    for a in range(0, T, 700):
+        assert torch.equal(bsq.moe_combine(y, p[a:a + 700].contiguous(), w[a:a + 700].contiguous()), many[a:a + 700])
+    # 2900 of the tokens dropped: the same rows of the first 100 from both gathers
+    x = gauss(T, H, seed=2).to(DEV)
+    e = ids(T, k, E, 22).to(DEV)
+    e[100:] = -1
+    few, all_ = bsq.moe_sort(e[:100].contiguous(), E, 32), bsq.moe_sort(e, E, 32)
+    for f in (bsq.moe_gather_mxfp8, bsq.moe_gather_nvfp4_rowscaled):
+        a = f(x[:100], few["positions"], few["source"])
+        b = f(x, all_["positions"], all_["source"])
+        n = min(few["source"].numel(), all_["source"].numel())
+        assert all(torch.equal(a[key][:n], b[key][:n]) for key in a)
+
+
+def test_on_another_stream():
+    T, k, E, H = 200, 2, 8, 256
+    e, x, w = ids(T, k, E, 1).to(DEV), gauss(T, H, seed=1).to(DEV), torch.rand((T, k), device=DEV)
+    o = bsq.moe_sort(e, E)
+    want = bsq.moe_combine(bsq.moe_gather(x, o["positions"], o["source"]), o["positions"], w)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        x2 = x * 2   # only the side stream's order makes it ready
+        o = bsq.moe_sort(e, E)
+        got = bsq.moe_combine(bsq.moe_gather(x2, o["positions"], o["source"]), o["positions"], w)
+    side.synchronize()
+    assert torch.equal(got, want * 2)
