@@ -700,10 +700,13 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
 
 # ---------------------------------------------------------------- tokens and their experts
 
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # the former without its Python around it
+
+
 def _call(fn: str, dev, *args):
     """The C entry point on dev's current stream, which may belong to another device than the current one."""
     f = getattr(lib(), fn)
-    if dev.index == torch.cuda.current_device():
+    if dev.index == _get_device():
         _check(fn, f(*args, _stream(dev)))
     else:
         with torch.cuda.device(dev):

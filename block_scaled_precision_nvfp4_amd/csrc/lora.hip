@@ -9,9 +9,9 @@
 //
 // Bound by memory where tokens are many (x once, y once each way), by latency where they are few.  us in a graph, states
 // rotating through 800 MB: 16 tokens of 16 adapters, rank 16, 4096 x 4096 6.5; 64 of one adapter, rank 64, 12.7;
-// 1024 in runs, rank 16, 14336 x 4096 28; 4096 in runs of 8 adapters, rank 64, 4096 x 4096 40 (down 17, up 23; its
-// bytes alone take 23 at the rate of a large copy), tokens of the same 8 adapters shuffled 153: every tile then has
-// most of them.
+// 1024 in runs, rank 16, 14336 x 4096 30; 4096 in runs of 8 adapters, rank 64, 4096 x 4096 39 (down 16, up 24; its
+// bytes alone take 23 at the rate of a large copy), with K 14336 65, tokens of the same 8 adapters
+// shuffled 144: every tile then has most of them.
 #include "launch.hpp"
 #include "lora.hpp"
 
@@ -55,7 +55,7 @@ __device__ __forceinline__ void lora_wave_fence() {
 
 template <int NR>
 __global__ __launch_bounds__(64 * lora_waves(NR)) void lora_down_kernel(LoraArgs a) {
-    constexpr int W = lora_waves(NR), D = NR == 1 ? 4 : 2, ROWS = LORA_TOKENS * (NR + 1);
+    constexpr int W = lora_waves(NR), D = NR == 1 ? 4 : NR == 2 ? 2 : 1, ROWS = LORA_TOKENS * (NR + 1);
     static_assert(W * NR * LORA_TOKENS * 17 * 4 <= W * ROWS * LORA_PITCH, "the join takes the rows' place");
     __shared__ __attribute__((aligned(16))) uint8_t lds[W * ROWS * LORA_PITCH];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -65,6 +65,8 @@ __global__ __launch_bounds__(64 * lora_waves(NR)) void lora_down_kernel(LoraArgs
     const int64_t m0 = (int64_t)tile * LORA_TOKENS;
     const int rank0 = blockIdx.z * 16 * NR, K = (int)a.K, pieces = (K + 63) / 64;
     const int ids = lora_ids(a, m0);
+    // tokens that no other workgroup reads pass the caches by, which A has for itself: 4096 tokens of 14336, rank 64, 70 -> 64 us
+    const bool once = gridDim.y == 1 && gridDim.z == 1;
     uint8_t* mine = lds + wave * ROWS * LORA_PITCH;
     for_adapters(ids, blockIdx.y, gridDim.y, [&](int id) {
         const uint32_t rows = (uint32_t)__ballot(ids == id) & 0xFFFFu;   // the tile's tokens with this adapter
@@ -81,7 +83,8 @@ __global__ __launch_bounds__(64 * lora_waves(NR)) void lora_down_kernel(LoraArgs
         auto load = [&](int d, int c) {
             if (64 * (c + 1) <= K) {
 #pragma unroll
-                for (int i = 0; i < 2 * (NR + 1); ++i) v[d][i] = *(const uint4*)(from[i] + 64 * c);
+                for (int i = 0; i < 2 * (NR + 1); ++i)
+                    v[d][i] = i < 2 && once ? load16_stream(from[i] + 64 * c) : *(const uint4*)(from[i] + 64 * c);
             } else {   // the piece that K ends in
 #pragma unroll
                 for (int i = 0; i < 2 * (NR + 1); ++i) {
@@ -328,15 +331,18 @@ __global__ __launch_bounds__(256) void lora_down_few_kernel(LoraArgs a, int rq) 
 
 int launch_lora_down_many(const LoraArgs& a, hipStream_t s) {
     const int64_t tiles = (a.M + LORA_TOKENS - 1) / LORA_TOKENS;
-    // a workgroup for each adapter that a tile can have while the tiles are few
-    const unsigned many = tiles <= 16 ? LORA_TOKENS : tiles < 256 ? (unsigned)(256 / tiles) : 1u;
-    if (a.r <= 16)
-        hipLaunchKernelGGL((lora_down_kernel<1>), dim3((unsigned)tiles, many, 1), dim3(64 * lora_waves(1)), 0, s, a);
-    else if (a.r <= 32)
-        hipLaunchKernelGGL((lora_down_kernel<2>), dim3((unsigned)tiles, many, 1), dim3(64 * lora_waves(2)), 0, s, a);
-    else
-        hipLaunchKernelGGL((lora_down_kernel<4>), dim3((unsigned)tiles, many, (unsigned)((a.r + 63) / 64)),
-                           dim3(64 * lora_waves(4)), 0, s, a);
+    // 64 ranks a workgroup, which then reads x once, or fewer while that leaves CUs idle; and a workgroup for each
+    // adapter that a tile may have while CUs are left even so.  us of the whole call with 64 ranks a workgroup and
+    // by this rule, tokens x 4096 x 4096 in runs, rank 64: 128 tokens 16.6 and 12.6, 256 21.4 and 15.0, 1024
+    // 24.7 and 18.8, 2048 29.2 and 24.5; 1024 tokens of 8 adapters shuffled, rank 32, 33 and 41.
+    int nr = 4;
+    while (nr > 1 && (16 * (nr / 2) >= a.r || tiles * ((a.r + 16 * nr - 1) / (16 * nr)) < 256)) nr /= 2;
+    const int64_t z = (a.r + 16 * nr - 1) / (16 * nr), many = 256 / (tiles * z);
+    const dim3 grid((unsigned)tiles, (unsigned)(many < 1 ? 1 : many > LORA_TOKENS ? LORA_TOKENS : many), (unsigned)z);
+    const dim3 block(64 * lora_waves(nr));
+    if (nr == 1) hipLaunchKernelGGL((lora_down_kernel<1>), grid, block, 0, s, a);
+    else if (nr == 2) hipLaunchKernelGGL((lora_down_kernel<2>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((lora_down_kernel<4>), grid, block, 0, s, a);
     return (int)hipGetLastError();
 }
 
