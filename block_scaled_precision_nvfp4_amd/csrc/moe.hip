@@ -7,7 +7,11 @@
 //   combine   out[t] = sum_j w[t][j] y[row of slot t k + j]
 //   backward  dy[row of slot i] = w_i dout[i / k],  dw_i = <dout[i / k], y[row of slot i]>
 //
-// None of them does arithmetic to speak of: a call is bound by the bytes of its rows, or by latency.
+// None of them does arithmetic to speak of: a call is bound by the bytes of its rows, or by latency.  us in a graph, with
+// several inputs in turn (the caches hold one): sort 37 x 2 slots of 8 experts 4.1, 16384 x 8 of 128 10.9 (two
+// launches); gather 16384 x 2 of 4096 bf16 70 (5.8 TB/s), 8191 x 8 of 2080 MXFP8 34 (5.2), 64 x 8 of 4096 NVFP4 3.4;
+// combination 1 x 2 of 4096 2.2, 16384 x 2 63 (6.4); its backward 16384 x 2 121 (5.6), 333 x 6 of 1032 fp32 6.1.  A
+// large copy runs at 4.8 to 4.9.
 #include "encode.hpp"
 #include "launch.hpp"
 
@@ -235,7 +239,7 @@ int launch_moe_sort(const void* experts, int id8, int64_t n, int64_t E, int64_t 
 // ---------------------------------------------------------------- rows without a slot
 
 // Waves at the end of a launch write zeros to the rows that no slot fills.  Wave w of `waves` looks at the rows w,
-// w + waves, ..., 64 at a time, so that a long stretch of such rows (behind the last group) is shared by all.
+// w + waves, ..., up to 64 at a time, so that a long stretch of such rows (behind the last group) is shared by all.
 template <class F>
 __device__ __forceinline__ void for_empty_rows(const int32_t* source, int64_t rows, int64_t slots, int64_t wave,
                                                int64_t waves, F&& zero) {
@@ -265,8 +269,9 @@ struct MoeSlots {
 
 // The rows of token t's slots, k <= 64 of them: lane j fetches slot j's, all in one trip to memory.  Fetched one after
 // another (for_slots with FEW false), each waits for a trip of its own; a full chip does not mind, and MXFP8 rows, and
-// a combination of few, do better so paced.  us with lanes and one after another: 64 tokens x 8 of 4096, MXFP8 4.2
-// and 5.1, combination 4.3 and 6.6; MXFP8 8192 x 8 of 2048 35.8 and 29.0, combination 16384 x 2 of 4096 65.8 and 61.0.
+// a combination of few, do better so paced.  us with lanes and one after another: 64 tokens x 8 of 4096, MXFP8 without
+// padding 4.2 and 5.1, combination 4.2 and 6.6; MXFP8 8192 x 8 of 2048 31.0 and 28.8, combination 16384 x 2 of 4096 64.7
+// and 62.5, 8192 x 8 of 2048 52.1 and 53.4.
 struct TokenRows {
     int32_t p;
     uint64_t left;   // slots that have a row, in ascending order
@@ -295,10 +300,11 @@ __device__ __forceinline__ void for_slots(const MoeSlots& s, int64_t t, F&& body
     }
 }
 
-// Stores of 16 bytes; with NT past the caches, for outputs that they could not hold until somebody reads them: half of
-// the memory-side cache or more, in rows of whole 128-byte lines (a line that two rows share would be written twice:
-// 45 us instead of 34 for MXFP8 rows of 2080 bytes).  us with and without, 402 and 670 MB moved: combination 60.9 and
-// 62.5, its backward 100 and 122, gather 69 and 75.
+// Stores of 16 bytes; with NT past the caches, for rows that they could not hold until somebody reads them: half of the
+// memory-side cache or more, in rows of whole 128-byte lines (a line that two rows share would be written twice: 45 us
+// instead of 34 for MXFP8 rows of 2080 bytes).  us with and without: gather of 402 MB 68 and 74, the combination's
+// backward of 671 MB 118 and 121, of 1208 MB with fp32 outputs 228 and 236; the combination, which writes in order, 63.6
+// and 63.0, has none.
 template <bool NT>
 __device__ __forceinline__ void put(void* p, const uint4 v) {
     if constexpr (NT) __builtin_nontemporal_store(u32v4{v.x, v.y, v.z, v.w}, (u32v4*)p);
@@ -347,9 +353,17 @@ __global__ __launch_bounds__(MOE_THREADS) void moe_gather_kernel(GatherArgs a) {
     }
 }
 
-static unsigned empty_groups(int64_t rows) {   // a wave for 64 rows, at most 1024 workgroups
-    const int64_t g = (rows + 64 * MOE_WAVES - 1) / (64 * MOE_WAVES);
-    return (unsigned)(g < 1 ? 1 : g > 1024 ? 1024 : g);
+// Workgroups for the rows without a slot: a wave for 4 rows up to one workgroup a CU, then for 64 up to four.  us with a
+// wave for 64 rows throughout, where most rows are padding: 4 tokens x 8 of 128 experts, bf16 4096 wide, 22 and now 4;
+// 64 x 8 MXFP8 16.8 and 5.7.  Of many rows few are empty, and every workgroup that looks for them costs: 66 thousand of
+// MXFP8 34.1, with 1024 workgroups 35.9.
+static unsigned empty_groups(int64_t rows) {
+    auto groups = [&](int64_t each, int64_t most) {
+        const int64_t g = (rows + each * MOE_WAVES - 1) / (each * MOE_WAVES);
+        return (unsigned)(g < 1 ? 1 : g > most ? most : g);
+    };
+    const unsigned few = groups(4, 256), many = groups(64, 1024);
+    return few > many ? few : many;
 }
 
 constexpr int GATHER_U = 4;   // vectors of a lane: 2 and 8 within 2 %
@@ -546,38 +560,50 @@ int launch_moe_gather_nvfp4(const void* x, int64_t ldx, int64_t T, int64_t k, in
 
 // ---------------------------------------------------------------- combine
 
-// Eight values of a row of experts' outputs.
+// A lane's part of 64 lanes' piece of a row: 16 bytes of the experts' outputs, 8 bf16 or 4 fp32 values, so that the
+// lanes of every access are neighbours.
 template <bool F32>
-struct Row8 {
-    uint4 q[F32 ? 2 : 1];
+struct Piece {
+    static constexpr int N = F32 ? 4 : 8;      // values of a lane
+    static constexpr int ALL = 64 * N;         // of the wave
+    uint4 q;
     __device__ __forceinline__ void load(const void* y, int64_t at) {
-        if constexpr (F32) {
-            q[0] = load16_stream((const float*)y + at);
-            q[1] = load16_stream((const float*)y + at + 4);
-        } else {
-            q[0] = load16_stream((const uint16_t*)y + at);
-        }
+        q = load16_stream((const uint8_t*)y + at * (F32 ? 4 : 2));
     }
-    __device__ __forceinline__ void values(float v[8]) const {
+    __device__ __forceinline__ void values(float (&v)[N]) const {
         if constexpr (F32) {
-            v[0] = __uint_as_float(q[0].x); v[1] = __uint_as_float(q[0].y);
-            v[2] = __uint_as_float(q[0].z); v[3] = __uint_as_float(q[0].w);
-            v[4] = __uint_as_float(q[1].x); v[5] = __uint_as_float(q[1].y);
-            v[6] = __uint_as_float(q[1].z); v[7] = __uint_as_float(q[1].w);
+            v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y);
+            v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
         } else {
-            unpack_bf16x8(q[0], v);
+            unpack_bf16x8(q, v);
         }
     }
 };
 
-template <bool F32, bool NT>
-__device__ __forceinline__ void store8(void* y, int64_t at, const float v[8]) {
-    if constexpr (F32) {
-        put<NT>((float*)y + at, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
-        put<NT>((float*)y + at + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
+// N = 4 or 8 bf16 values.
+template <int N>
+__device__ __forceinline__ void load_bf16(const uint16_t* p, float (&v)[N]) {
+    if constexpr (N == 8) {
+        unpack_bf16x8(*(const uint4*)p, v);
     } else {
+        const uint2 q = *(const uint2*)p;
+        v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x);
+        v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
+    }
+}
+
+template <bool F32, bool NT, int N>
+__device__ __forceinline__ void store_row(void* y, int64_t at, const float (&v)[N]) {
+    if constexpr (F32) {
+#pragma unroll
+        for (int e = 0; e < N; e += 4)
+            put<NT>((float*)y + at + e, make_uint4(__float_as_uint(v[e]), __float_as_uint(v[e + 1]), __float_as_uint(v[e + 2]),
+                                                   __float_as_uint(v[e + 3])));
+    } else if constexpr (N == 8) {
         put<NT>((uint16_t*)y + at,
                 make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7])));
+    } else {
+        *(uint2*)((uint16_t*)y + at) = make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
     }
 }
 
@@ -590,18 +616,19 @@ struct CombineArgs {
 };
 
 // Sums in fp32 over j in ascending order, one rounding to the output's type.
-template <bool YF32, bool OF32, bool NT, bool FEW>
+template <bool YF32, bool OF32, bool FEW>
 __global__ __launch_bounds__(MOE_THREADS) void moe_combine_kernel(CombineArgs a) {
+    typedef Piece<YF32> P;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int64_t pieces = (a.H + 511) / 512;
-    const int64_t u = (int64_t)blockIdx.x * MOE_WAVES + wave, t = u / pieces, c = (u % pieces) * 512 + 8 * lane;
+    const int64_t pieces = (a.H + P::ALL - 1) / P::ALL, group = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    const int64_t u = group * MOE_WAVES + wave, t = u / pieces, c = (u % pieces) * P::ALL + P::N * lane;
     if (t >= a.s.T) return;
-    float acc[8] = {};
-    auto add = [&](float w, const Row8<YF32>& q) {
-        float y[8];
+    float acc[P::N] = {};
+    auto add = [&](float w, const P& q) {
+        float y[P::N];
         q.values(y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(w, y[e], acc[e]);
+        for (int e = 0; e < P::N; ++e) acc[e] = __builtin_fmaf(w, y[e], acc[e]);
     };
     if constexpr (FEW) {
         constexpr int G = 4;   // rows in flight
@@ -609,7 +636,7 @@ __global__ __launch_bounds__(MOE_THREADS) void moe_combine_kernel(CombineArgs a)
         const float weight = a.weights && lane < a.s.k ? a.weights[t * a.s.k + lane] : 1.0f;   // of slot `lane`
         while (rows.left) {
             float w[G];
-            Row8<YF32> q[G];
+            P q[G];
             int n = 0;
 #pragma unroll
             for (int u = 0; u < G; ++u)
@@ -627,12 +654,12 @@ __global__ __launch_bounds__(MOE_THREADS) void moe_combine_kernel(CombineArgs a)
     } else {
         if (c >= a.H) return;
         for_slots<false>(a.s, t, [&](int j, int64_t r) {
-            Row8<YF32> q;
+            P q;
             q.load(a.y, r * a.H + c);
             add(a.weights ? a.weights[t * a.s.k + j] : 1.0f, q);
         });
     }
-    store8<OF32, NT>(a.out, t * a.H + c, acc);
+    store_row<OF32, false>(a.out, t * a.H + c, acc);
 }
 
 int launch_moe_combine(const void* y, int y_f32, int64_t T, int64_t k, int64_t H, const int32_t* positions, int64_t rows,
@@ -640,18 +667,19 @@ int launch_moe_combine(const void* y, int y_f32, int64_t T, int64_t k, int64_t H
     if (T == 0 || H == 0) return 0;
     hipStream_t s = (hipStream_t)hip_stream;
     const CombineArgs a{y, H, {positions, nullptr, T, (int)k, rows}, weights, out};
-    const int64_t waves = T * ((H + 511) / 512);
-    const dim3 grid((unsigned)((waves + MOE_WAVES - 1) / MOE_WAVES)), block(MOE_THREADS);
-    auto launch = [&](auto nt_c, auto few_c) {
-        constexpr bool NT = decltype(nt_c)::value, FEW = decltype(few_c)::value;
-        if (y_f32 && out_f32) hipLaunchKernelGGL((moe_combine_kernel<true, true, NT, FEW>), grid, block, 0, s, a);
-        else if (y_f32) hipLaunchKernelGGL((moe_combine_kernel<true, false, NT, FEW>), grid, block, 0, s, a);
-        else if (out_f32) hipLaunchKernelGGL((moe_combine_kernel<false, true, NT, FEW>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((moe_combine_kernel<false, false, NT, FEW>), grid, block, 0, s, a);
+    const int64_t width = y_f32 ? Piece<true>::ALL : Piece<false>::ALL, waves = T * ((H + width - 1) / width);
+    const int64_t groups = (waves + MOE_WAVES - 1) / MOE_WAVES;   // fp32 rows: up to 2^24, a thread more than x holds
+    const unsigned high = groups > (int64_t)1 << 23 ? 2 : 1;
+    const dim3 grid((unsigned)((groups + high - 1) / high), high), block(MOE_THREADS);
+    auto launch = [&](auto few_c) {
+        constexpr bool FEW = decltype(few_c)::value;
+        if (y_f32 && out_f32) hipLaunchKernelGGL((moe_combine_kernel<true, true, FEW>), grid, block, 0, s, a);
+        else if (y_f32) hipLaunchKernelGGL((moe_combine_kernel<true, false, FEW>), grid, block, 0, s, a);
+        else if (out_f32) hipLaunchKernelGGL((moe_combine_kernel<false, true, FEW>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((moe_combine_kernel<false, false, FEW>), grid, block, 0, s, a);
     };
-    if (past_caches(T, H * (out_f32 ? 4 : 2))) launch(std::true_type{}, std::false_type{});
-    else if (few_tokens(waves)) launch(std::false_type{}, std::true_type{});
-    else launch(std::false_type{}, std::false_type{});
+    if (few_tokens(waves)) launch(std::true_type{});
+    else launch(std::false_type{});
     return (int)hipGetLastError();
 }
 
@@ -667,15 +695,16 @@ struct CombineBwdArgs {
 };
 
 // A wave takes a slot: the token's row of dout (which the waves of its other slots read about the same time, so that it
-// comes from memory once) with the slot's row of y, U pieces of 512 elements at a time.
+// comes from memory once) with the slot's row of y, U pieces of it at a time.
 template <bool YF32, int U, bool NT>
 __global__ __launch_bounds__(MOE_THREADS) void moe_combine_backward_kernel(CombineBwdArgs a) {
+    typedef Piece<YF32> P;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     if (blockIdx.x >= a.token_groups) {
         const int64_t w = (int64_t)(blockIdx.x - a.token_groups) * MOE_WAVES + wave;
         for_empty_rows(a.s.source, a.s.rows, a.s.T * a.s.k, w, (int64_t)(gridDim.x - a.token_groups) * MOE_WAVES, [&](int64_t r) {
-            const float zero[8] = {};
-            for (int64_t c = 8 * lane; c < a.H; c += 512) store8<YF32, NT>(a.dy, r * a.H + c, zero);
+            const float zero[P::N] = {};
+            for (int64_t c = P::N * lane; c < a.H; c += P::ALL) store_row<YF32, NT>(a.dy, r * a.H + c, zero);
         });
         return;
     }
@@ -689,27 +718,26 @@ __global__ __launch_bounds__(MOE_THREADS) void moe_combine_backward_kernel(Combi
     }
     const float w = a.weights[i];
     float dot = 0.0f;
-    for (int64_t c0 = 8 * lane; c0 < a.H; c0 += 512 * U) {
-        uint4 d[U];
-        Row8<YF32> q[U];
+    for (int64_t c0 = P::N * lane; c0 < a.H; c0 += P::ALL * U) {
+        float d[U][P::N];
+        P q[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (c0 + 512 * u < a.H) {
-                q[u].load(a.y, (int64_t)r * a.H + c0 + 512 * u);
-                d[u] = *(const uint4*)(a.dout + t * a.H + c0 + 512 * u);
+            if (c0 + P::ALL * u < a.H) {
+                q[u].load(a.y, (int64_t)r * a.H + c0 + P::ALL * u);
+                load_bf16(a.dout + t * a.H + c0 + P::ALL * u, d[u]);
             }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (c0 + 512 * u < a.H) {
-                float x[8], v[8];
-                unpack_bf16x8(d[u], x);
+            if (c0 + P::ALL * u < a.H) {
+                float v[P::N];
                 q[u].values(v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    dot = __builtin_fmaf(x[e], v[e], dot);
-                    x[e] = w * x[e];
+                for (int e = 0; e < P::N; ++e) {
+                    dot = __builtin_fmaf(d[u][e], v[e], dot);
+                    d[u][e] = w * d[u][e];
                 }
-                store8<YF32, NT>(a.dy, (int64_t)r * a.H + c0 + 512 * u, x);
+                store_row<YF32, NT>(a.dy, (int64_t)r * a.H + c0 + P::ALL * u, d[u]);
             }
     }
 #pragma unroll

@@ -480,3 +480,15 @@ def test_on_another_stream():
         got = bsq.moe_combine(bsq.moe_gather(x2, o["positions"], o["source"]), o["positions"], w)
     side.synchronize()
     assert torch.equal(got, want * 2)
+
+
+def test_combination_of_the_most_tokens():
+    """The largest call: 2^23 tokens of 2048, fp32 rows, one slot each."""
+    T, H, rows = 1 << 23, 2048, 64
+    y = gauss(rows, H, seed=3, dtype=torch.float32).to(DEV)
+    p = (torch.arange(T, dtype=torch.int32, device=DEV) * 7 % (rows + 1)).reshape(T, 1)   # row 64 is out of range
+    note("combine %d x %d" % (T, H))
+    out = bsq.moe_combine(y, p)
+    want = torch.cat([y, torch.zeros(1, H, device=DEV)]).to(torch.bfloat16)
+    for t0 in range(0, T, 1 << 20):
+        assert torch.equal(out[t0:t0 + (1 << 20)], want[p[t0:t0 + (1 << 20), 0].long()])
