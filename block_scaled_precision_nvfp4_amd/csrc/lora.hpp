@@ -22,7 +22,6 @@ struct LoraArgs {
     int64_t ldy;
     void* out;
     int64_t ldo;
-    bool vec;                   // 4 columns of y and out are one aligned access, from every 4th on
 };
 
 __host__ __device__ constexpr int lora_steps(int r) { return (r + 31) / 32; }

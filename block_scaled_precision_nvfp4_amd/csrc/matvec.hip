@@ -551,7 +551,7 @@ int launch_nvfp4_lora_matvec(const void* x, int64_t ldx, int64_t M, int64_t N, i
     void* sum = y_f32 ? y : base;
     MvArgs a{(const uint16_t*)x, ldx, M, N, K, {{w_codes, w_scales, w_s_enc}, {}}, rows, sum, 1, -1, 1, {}, 0, 0, 0};
     a.lora = LoraArgs{M, N, K, (int)r, L, a.x, ldx, adapters, (const uint16_t*)lora_a, (const uint16_t*)lora_b, scales,
-                      down, sum, N, y, N, N % 4 == 0};
+                      down, sum, N, y, N};
     int e;
     if (M <= LORA_FEW) {
         e = launch_any<false, true>(a, s);

@@ -8,7 +8,7 @@
 //   backward  dy[row of slot i] = w_i dout[i / k],  dw_i = <dout[i / k], y[row of slot i]>
 //
 // None of them does arithmetic to speak of: a call is bound by the bytes of its rows, or by latency.  us in a graph, with
-// several inputs in turn (the caches hold one): sort 37 x 2 slots of 8 experts 4.1, 16384 x 8 of 128 10.9 (two
+// several inputs in turn (the caches hold one): sort 37 x 2 slots of 8 experts 3.8, 16384 x 8 of 128 11.0 (two
 // launches); gather 16384 x 2 of 4096 bf16 70 (5.8 TB/s), 8191 x 8 of 2080 MXFP8 34 (5.2), 64 x 8 of 4096 NVFP4 3.4;
 // combination 1 x 2 of 4096 2.2, 16384 x 2 63 (6.4); its backward 16384 x 2 121 (5.6), 333 x 6 of 1032 fp32 6.1.  A
 // large copy runs at 4.8 to 4.9.
@@ -183,9 +183,10 @@ __global__ __launch_bounds__(64 * SORT_WAVES) void moe_place_kernel(SortArgs a) 
         }
     }
     // rows of no slot: the groups' padding, and what lies behind the last group
-    for (int e = blockIdx.x + gridDim.x * wave; e < E; e += gridDim.x * waves) {
-        const int end = e + 1 < E ? start[e + 1] : base;
-        for (int r = start[e] + total[e] + lane; r < end; r += 64) a.source[r] = -1;
+    const int shift = __builtin_ctz(a.align);
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < (int64_t)E << shift; i += (int64_t)gridDim.x * blockDim.x) {
+        const int e = (int)(i >> shift), r = start[e] + total[e] + (int)(i & (a.align - 1));
+        if (r < (e + 1 < E ? start[e + 1] : base)) a.source[r] = -1;
     }
     for (int64_t r = base + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < a.rows; r += (int64_t)gridDim.x * blockDim.x)
         a.source[r] = -1;
@@ -194,7 +195,8 @@ __global__ __launch_bounds__(64 * SORT_WAVES) void moe_place_kernel(SortArgs a) 
 // The launch's shape: one workgroup up to 4096 slots, of as many waves as have slots; else a count first, and
 // several workgroups, each wave with 64 slots or, where that would be over 128 workgroups, more.  us in a graph, one
 // workgroup and several, 8 / 128 experts: 2048 slots 6.1 / 7.7 and 8.2 / 9.3, 4096 7.5 / 9.8 and 8.2 / 9.1 (a
-// second launch costs the host 2), 16384 16.2 / 22.1 and 8.4 / 9.6; with 128 slots a wave 9.5 / 11.1.
+// second launch costs the host 2), 16384 16.2 / 22.1 and 8.4 / 9.6; with 128 slots a wave 9.5 / 11.1.  A few slots of
+// many experts take a wave for 16 experts too, which share their counts: 4 x 5 of 63, padded to 32, 7.0 and 5.1.
 constexpr int SORT_ONE = 4096, SORT_MINE = 64;
 
 struct SortShape {
@@ -206,7 +208,7 @@ static SortShape sort_shape(int64_t n, int64_t E) {
     int waves = SORT_WAVES;
     while (waves * E > SORT_HIST) waves /= 2;
     if (n <= SORT_ONE) {
-        while (waves > 1 && waves / 2 * 64 >= n) waves /= 2;
+        while (waves > 1 && waves / 2 * 64 >= n && waves / 2 * 16 >= E) waves /= 2;
         const int64_t lanes = 64 * waves;
         return {1, (n + lanes - 1) / lanes * 64, waves};
     }

@@ -331,3 +331,23 @@ def test_no_token_with_an_adapter(M):
         assert torch.equal(got.view(torch.uint8), before.view(torch.uint8))
         bsq.lora_add(y, x, ad, a, b, s)
         assert torch.equal(y.view(torch.uint8), before.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N", [1, 2, 3, 61, 62, 63, 64, 65, 66, 67, 190])
+def test_ends_of_rows_at_any_alignment(N, dtype):
+    """Every number of columns past a piece, in a slice of a wider y that starts and continues at odd elements: the bits of
+    the same columns of a wide call, and nothing beside the slice."""
+    M, K, r, L, W = 83, 96, 24, 3, 192
+    x, ad, a, b, s = case(M, W, K, r, L, seed=4)
+    y = gauss(M, W, seed=9, dtype=dtype)
+    want = bsq.lora_add(y, x, ad, a, b, s, out=torch.empty_like(y))[:, :N]
+    for left in (0, 1, 3):
+        wide = gauss(M, left + N + 2 - (left + N) % 2 + 1, seed=2, dtype=dtype)   # an odd number of elements between rows
+        wide[:, left:left + N] = y[:, :N]
+        before, out = wide.clone(), wide.clone()
+        bsq.lora_add(wide[:, left:left + N], x, ad, a, b[:, :N].contiguous(), s, out=out[:, left:left + N])
+        bsq.lora_add(wide[:, left:left + N], x, ad, a, b[:, :N].contiguous(), s)
+        for t in (out, wide):
+            assert torch.equal(t[:, left:left + N], want)
+            assert torch.equal(t[:, :left], before[:, :left]) and torch.equal(t[:, left + N:], before[:, left + N:])

@@ -492,3 +492,10 @@ def test_combination_of_the_most_tokens():
     want = torch.cat([y, torch.zeros(1, H, device=DEV)]).to(torch.bfloat16)
     for t0 in range(0, T, 1 << 20):
         assert torch.equal(out[t0:t0 + (1 << 20)], want[p[t0:t0 + (1 << 20), 0].long()])
+
+
+@pytest.mark.parametrize("T,k,E", [(6, 4, 126), (4, 5, 63), (1, 8, 1024), (2, 1, 17), (64, 8, 128), (65, 3, 33)])
+@pytest.mark.parametrize("align", [1, 16, 256])
+def test_sort_of_few_slots_for_many_experts(T, k, E, align):
+    check_sort(ids(T, k, E, T + E), E, align)
+    check_sort(ids(T, k, E, T + E, drop=0.3, dtype=torch.int32), E, align)
