@@ -8,7 +8,7 @@
 // NaN stays with its token, or its adapter's tokens.
 //
 // Bound by memory where tokens are many (x once, y once each way), by latency where they are few.  us in a graph, states
-// rotating through 800 MB: 16 tokens of 16 adapters, rank 16, 4096 x 4096 6.5; 64 of one adapter, rank 64, 12.7;
+// rotating through 800 MB: 16 tokens of 16 adapters, rank 16, 4096 x 4096 6.4; 64 of one adapter, rank 64, 11.1;
 // 1024 in runs, rank 16, 14336 x 4096 30; 4096 in runs of 8 adapters, rank 64, 4096 x 4096 39 (down 16, up 24; its
 // bytes alone take 23 at the rate of a large copy), with K 14336 65, tokens of the same 8 adapters
 // shuffled 144: every tile then has most of them.
@@ -339,12 +339,64 @@ __global__ __launch_bounds__(64 * LORA_UP_WAVES) void lora_up_kernel(LoraArgs a,
     }
 }
 
-// Few tokens: a thread takes one value of y, so that any mixture of adapters goes at once.
-template <bool YF, bool OF>
+// Few tokens: a wave takes some columns of one, so that any mixture of adapters goes at once.  G lanes share a row of B,
+// 16 bytes each, and 64 / G neighbouring rows are a load; the sums of I loads are then added up across the G lanes in
+// halves, which leaves the lanes with a column each.  (A lane with a row of its own touches a line with each load.)  No
+// more than 4 loads: a wave runs through its code once, and every line of that comes from memory too.  us, against a
+// row for each lane: 64 tokens of 64 adapters, rank 64, 4096 x 4096, 19.1 and 25.6; one token, rank 256, 6.8 and 13.2 (7.6
+// with 8 loads, 22 with 32).
+constexpr int lora_few_loads(int lanes) { return lanes < 4 ? lanes : 4; }
+
+// G: lanes of a row, a power of two, 8 G >= r.
+template <bool YF, bool OF, int G>
 __global__ __launch_bounds__(256) void lora_up_few_kernel(LoraArgs a) {
-    const int64_t m = blockIdx.y, n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    constexpr int I = lora_few_loads(G), C = I * (64 / G);   // columns of a wave
+    const int lane = threadIdx.x & 63, pos = lane & (G - 1), sub = lane / G;
+    const int64_t m = blockIdx.y, n0 = ((int64_t)blockIdx.x * 4 + threadIdx.x / 64) * C, n = n0 + pos / (G / I) * (64 / G) + sub;
     const int id = a.adapters[m];
-    if (n < a.N && (a.out != a.y || (id >= 0 && id < a.L))) lora_store<OF>(a, m, n, lora_added(a, m, n, lora_y<YF>(a, m, n)));
+    const bool has = id >= 0 && id < a.L;
+    if (n0 >= a.N || (!has && a.out == a.y)) return;
+    float y = 0.0f;
+    if (n < a.N) y = lora_y<YF>(a, m, n);
+    if (has) {
+        const bool in = 8 * pos < a.r;
+        float t[8] = {};
+        if (in) {
+            const float4 t0 = *(const float4*)(a.t + m * a.r + 8 * pos), t1 = *(const float4*)(a.t + m * a.r + 8 * pos + 4);
+            t[0] = t0.x; t[1] = t0.y; t[2] = t0.z; t[3] = t0.w;
+            t[4] = t1.x; t[5] = t1.y; t[6] = t1.z; t[7] = t1.w;
+        }
+        const uint16_t* b = a.b + (int64_t)id * a.N * a.r + (in ? 8 * pos : 0);
+        uint4 v[I];
+#pragma unroll
+        for (int i = 0; i < I; ++i) {   // of column n0 + i (64 / G) + sub, or the last one, whose sum nobody takes
+            const int64_t c = n0 + i * (64 / G) + sub;
+            v[i] = *(const uint4*)(b + (c < a.N ? c : a.N - 1) * a.r);
+        }
+        float s[I];
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            const uint4 q = in ? v[i] : make_uint4(0, 0, 0, 0);
+            float w[8];
+            unpack_bf16x8(q, w);
+            s[i] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[i] = __builtin_fmaf(t[e], w[e], s[i]);
+        }
+#pragma unroll
+        for (int h = G / 2; h > 0; h /= 2) {
+            const int half = h * I / G;   // sums that a lane keeps
+#pragma unroll
+            for (int i = 0; i < half; ++i) {
+                const bool high = pos & h;
+                const float other = __shfl_xor(high ? s[i] : s[i + half], h);
+                s[i] = (high ? s[i + half] : s[i]) + other;
+            }
+            if (half == 0) s[0] += __shfl_xor(s[0], h);
+        }
+        y = __builtin_fmaf(a.scales ? a.scales[id] : 1.0f, s[0], y);
+    }
+    if (n < a.N && pos % (G / I) == 0) lora_store<OF>(a, m, n, y);
 }
 
 __global__ __launch_bounds__(256) void lora_down_few_kernel(LoraArgs a, int rq) {
@@ -376,7 +428,16 @@ int64_t lora_up_groups(int64_t M, int64_t N) {
 template <bool YF, bool OF>
 static int launch_up(const LoraArgs& a, hipStream_t s) {
     if (a.M <= LORA_FEW) {
-        hipLaunchKernelGGL((lora_up_few_kernel<YF, OF>), dim3((unsigned)((a.N + 255) / 256), (unsigned)a.M), dim3(256), 0, s, a);
+        auto launch = [&](auto lanes) {
+            constexpr int G = decltype(lanes)::value, C = 4 * lora_few_loads(G) * (64 / G);
+            hipLaunchKernelGGL((lora_up_few_kernel<YF, OF, G>), dim3((unsigned)((a.N + C - 1) / C), (unsigned)a.M), dim3(256), 0, s, a);
+        };
+        if (a.r <= 8) launch(std::integral_constant<int, 1>{});
+        else if (a.r <= 16) launch(std::integral_constant<int, 2>{});
+        else if (a.r <= 32) launch(std::integral_constant<int, 4>{});
+        else if (a.r <= 64) launch(std::integral_constant<int, 8>{});
+        else if (a.r <= 128) launch(std::integral_constant<int, 16>{});
+        else launch(std::integral_constant<int, 32>{});
         return (int)hipGetLastError();
     }
     const int64_t cols = (a.N + LORA_COLS - 1) / LORA_COLS, tiles = lora_up_groups(a.M, LORA_COLS);

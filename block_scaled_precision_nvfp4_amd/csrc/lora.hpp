@@ -102,27 +102,4 @@ __device__ __forceinline__ void lora_down_few(const LoraArgs& a, int rq, int64_t
 int launch_lora_down_many(const LoraArgs& a, hipStream_t s);
 int launch_lora_up(const LoraArgs& a, int y_f32, int out_f32, hipStream_t s);
 
-// y + s_a sum_q t[m][q] B_a[n][q] of token m's adapter a, in fp32; y where it has none.
-__device__ __forceinline__ float lora_added(const LoraArgs& a, int64_t m, int64_t n, float y) {
-    const int id = a.adapters[m];
-    if (id < 0 || id >= a.L) return y;
-    const uint16_t* b = a.b + ((int64_t)id * a.N + n) * a.r;
-    const float* t = a.t + m * a.r;
-    float s = 0.0f;
-    for (int q = 0; q < a.r; q += 8) {
-        float w[8];
-        unpack_bf16x8(*(const uint4*)(b + q), w);
-        const float4 t0 = *(const float4*)(t + q), t1 = *(const float4*)(t + q + 4);
-        s = __builtin_fmaf(t0.x, w[0], s);
-        s = __builtin_fmaf(t0.y, w[1], s);
-        s = __builtin_fmaf(t0.z, w[2], s);
-        s = __builtin_fmaf(t0.w, w[3], s);
-        s = __builtin_fmaf(t1.x, w[4], s);
-        s = __builtin_fmaf(t1.y, w[5], s);
-        s = __builtin_fmaf(t1.z, w[6], s);
-        s = __builtin_fmaf(t1.w, w[7], s);
-    }
-    return __builtin_fmaf(a.scales ? a.scales[id] : 1.0f, s, y);
-}
-
 }  // namespace bsq
