@@ -403,6 +403,12 @@ __global__ __launch_bounds__(256) void lora_down_few_kernel(LoraArgs a, int rq) 
     lora_down_few(a, rq, (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)));
 }
 
+int launch_lora_down_few(const LoraArgs& a, hipStream_t s) {
+    const int rq = lora_few_rows(a.M, a.r);
+    hipLaunchKernelGGL(lora_down_few_kernel, dim3((unsigned)((lora_few_units(a.M, a.r, rq) + 3) / 4)), dim3(256), 0, s, a, rq);
+    return (int)hipGetLastError();
+}
+
 int launch_lora_down_many(const LoraArgs& a, hipStream_t s) {
     const int64_t tiles = (a.M + LORA_TOKENS - 1) / LORA_TOKENS;
     // 64 ranks a workgroup, which then reads x once, or fewer while that leaves CUs idle; and a workgroup for each
@@ -471,14 +477,7 @@ int launch_lora_add(int f32, int64_t M, int64_t N, int64_t K, int64_t r, int64_t
     hipStream_t s = (hipStream_t)hip_stream;
     const LoraArgs a{M, N, K, (int)r, L, (const uint16_t*)x, ldx, adapters, (const uint16_t*)lora_a, (const uint16_t*)lora_b,
                      scales, workspace, y, ldy, out, ldo};
-    int e;
-    if (M <= LORA_FEW) {
-        const int rq = lora_few_rows(M, a.r);
-        hipLaunchKernelGGL(lora_down_few_kernel, dim3((unsigned)((lora_few_units(M, a.r, rq) + 3) / 4)), dim3(256), 0, s, a, rq);
-        e = (int)hipGetLastError();
-    } else {
-        e = launch_lora_down_many(a, s);
-    }
+    const int e = M <= LORA_FEW ? launch_lora_down_few(a, s) : launch_lora_down_many(a, s);
     return e ? e : launch_lora_up(a, f32, f32, s);
 }
 

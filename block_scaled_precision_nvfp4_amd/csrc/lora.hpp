@@ -98,7 +98,8 @@ __device__ __forceinline__ void lora_down_few(const LoraArgs& a, int rq, int64_t
     else lora_down_few_rows<4, 2>(a, unit);
 }
 
-// Both in lora.hip: the down products of any number of tokens, and the up products onto y.
+// In lora.hip: the down products of up to LORA_FEW tokens and of more, and the up products onto y.
+int launch_lora_down_few(const LoraArgs& a, hipStream_t s);
 int launch_lora_down_many(const LoraArgs& a, hipStream_t s);
 int launch_lora_up(const LoraArgs& a, int y_f32, int out_f32, hipStream_t s);
 

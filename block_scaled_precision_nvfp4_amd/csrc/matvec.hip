@@ -503,7 +503,20 @@ static int launch_tokens(MvArgs a, hipStream_t s) {
     while (a.wr < 4 && a.wr * MV_CUS < blocks * mb) a.wr *= 2;
     int parts = mv_waves(T) / a.wr < mv_parts(T) ? mv_waves(T) / a.wr : mv_parts(T);
     while (parts > 1 && parts / 2 >= chunks) parts /= 2;
-    if (LORA) mv_downs(a, a.wr * parts, mb);
+    if constexpr (LORA) {
+        mv_downs(a, a.wr * parts, mb);
+        const int64_t own = (blocks + a.wr - 1) / a.wr * mb;
+        auto rounds = [](int64_t groups) { return (groups + MV_CUS - 1) / MV_CUS; };
+        // From 16 tokens on a workgroup has a CU to itself, and down products that begin another round of them wait, or
+        // make weights wait, for a whole one: they go first, in a launch of their own.  Rank 16, us together and
+        // so: 16 x 4096 x 14336 37.8 and 30.2, 16 x 8192 x 4096 21.8 and 19.1; tiles of 64 tokens, 64 x 14336 x 4096 of
+        // rank 64, 43.7 and 45.0.  Past four rounds one more is no longer than that launch.
+        if (T >= 16 && T < 64 && rounds(own) < 4 && rounds(own + a.downs * mb) > rounds(own)) {
+            const int e = launch_lora_down_few(a.lora, s);
+            a.downs = 0;
+            return e ? e : launch_tokens<T, GATED, LOAD, false>(a, s);
+        }
+    }
     hipLaunchKernelGGL((matvec_tokens_kernel<T, GATED, LOAD, LORA>), dim3((unsigned)(a.downs + (blocks + a.wr - 1) / a.wr), (unsigned)mb),
                        dim3(64 * a.wr * parts), 0, s, a);
     return (int)hipGetLastError();
