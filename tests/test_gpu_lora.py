@@ -351,3 +351,28 @@ def test_ends_of_rows_at_any_alignment(N, dtype):
         for t in (out, wide):
             assert torch.equal(t[:, left:left + N], want)
             assert torch.equal(t[:, :left], before[:, :left]) and torch.equal(t[:, left + N:], before[:, left + N:])
+
+
+@pytest.mark.parametrize("M,N,K,r,L", [(16, 4096, 272, 16, 5), (5, 4090, 528, 128, 3), (20, 4111, 96, 8, 2), (33, 8192, 80, 64, 40)])
+def test_matvec_that_fills_the_chip(M, N, K, r, L):
+    """Weights that leave no compute unit idle: the down products go first."""
+    test_matvec(M, N, K, r, L, False)
+
+
+def test_replays_of_a_matvec_that_fills_the_chip():
+    M, N, K, r, L = 16, 4096, 512, 16, 5
+    x, ad, a, b, s = case(M, N, K, r, L, seed=3)
+    w = weights(N, K, 4)
+    bsq.nvfp4_lora_matvec(x, *w, ad, a, b, s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = bsq.nvfp4_lora_matvec(x, *w, ad, a, b, s)
+    for seed in range(4):
+        x.copy_(gauss(M, K, seed=50 + seed))
+        ad.copy_(adapters(M, L, 60 + seed, 0.2))
+        want = bsq.nvfp4_lora_matvec(x, *w, ad, a, b, s)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
