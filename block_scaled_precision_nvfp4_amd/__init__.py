@@ -4,7 +4,7 @@ Thin ctypes marshalling over the C ABI in include/bsq.h: every step of the compu
 runs in the library's HIP kernels.  PyTorch only provides device memory (output
 tensors are allocated with torch.empty) and the current HIP stream.  The functions
 have the names of the C entry points and are not recorded by autograd: results have no
-history.  Importing works without a GPU; calling a
+history, and a tensor of the caller that a call writes counts as changed.  Importing works without a GPU; calling a
 compute function needs libbsq.so (built by ``python -m
 block_scaled_precision_nvfp4_amd.build``) and fails loudly if it is missing.
 """
@@ -149,6 +149,15 @@ def _workspace(ws: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
     if not ws.is_contiguous() or ws.numel() * ws.element_size() < nbytes:
         raise ValueError("workspace must be contiguous and hold at least %d bytes" % nbytes)
     return ws
+
+
+def _written(*tensors: Optional[torch.Tensor]):
+    """Tensors of the caller that a call has written count as changed (their version counters), as after torch's own operators
+    in place: a backward pass that saved one says so instead of using what it holds now.  The kernels write through
+    pointers, which torch does not see.  None stands for a tensor that the call made itself."""
+    given = [t for t in tensors if t is not None]
+    if given:
+        torch.autograd.graph.increment_version(given)
 
 
 def _signs(rht_signs, device):
@@ -350,15 +359,16 @@ def blockscaled_gemm(fmt: int, a_codes: torch.Tensor, a_scales: torch.Tensor, a_
         raise ValueError("operands disagree on K")
     c_dtype = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}[out_dtype]
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a_codes.device)
+        c = torch.empty((M, N), dtype=out_dtype, device=a_codes.device)
     else:
-        _dev_tensor(out, out_dtype, "out")
+        c = _dev_tensor(out, out_dtype, "out")
         if tuple(out.shape) != (M, N):
             raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), (M, N)))
     _check("blockscaled_gemm", lib().blockscaled_gemm(
         fmt, M, N, K, a_codes.data_ptr(), a_scales.data_ptr(), _ptr(a_s_enc), b_codes.data_ptr(),
-        b_scales.data_ptr(), _ptr(b_s_enc), out.data_ptr(), c_dtype, _stream(a_codes.device)))
-    return out
+        b_scales.data_ptr(), _ptr(b_s_enc), c.data_ptr(), c_dtype, _stream(a_codes.device)))
+    _written(out)
+    return c
 
 
 def blockscaled_grouped_gemm(fmt: int, mode: int, offsets: torch.Tensor, a_codes: torch.Tensor,
@@ -392,15 +402,16 @@ def blockscaled_grouped_gemm(fmt: int, mode: int, offsets: torch.Tensor, a_codes
         raise ValueError("operands disagree on K")
     c_dtype = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}[out_dtype]
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=a_codes.device)
+        c = torch.empty(shape, dtype=out_dtype, device=a_codes.device)
     else:
-        _dev_tensor(out, out_dtype, "out")
+        c = _dev_tensor(out, out_dtype, "out")
         if tuple(out.shape) != shape:
             raise ValueError("out has shape %s, expected %s" % (tuple(out.shape), shape))
     _check("blockscaled_grouped_gemm", lib().blockscaled_grouped_gemm(
         fmt, mode, G, offsets.data_ptr(), M, N, K, a_codes.data_ptr(), a_scales.data_ptr(), _ptr(a_s_enc),
-        b_codes.data_ptr(), b_scales.data_ptr(), _ptr(b_s_enc), out.data_ptr(), c_dtype, _stream(a_codes.device)))
-    return out
+        b_codes.data_ptr(), b_scales.data_ptr(), _ptr(b_s_enc), c.data_ptr(), c_dtype, _stream(a_codes.device)))
+    _written(out)
+    return c
 
 
 def nvfp4_linear_forward(x: torch.Tensor, w: torch.Tensor, sr_seed: int, rht_signs,
@@ -489,11 +500,12 @@ def nvfp4_matvec(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
     dev = x.device
     N, rows = _weights(w_codes, w_scales, w_s_enc, K, "w", dev)
     y_dtype = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}[out_dtype]
-    out = _output(out, (M, N), out_dtype, dev)
+    y = _output(out, (M, N), out_dtype, dev)
     _check("nvfp4_matvec", lib().nvfp4_matvec(
         FMT_B_ROWSCALED if rows else 0, M, N, K, x.data_ptr(), ldx, w_codes.data_ptr(), w_scales.data_ptr(),
-        w_s_enc.data_ptr(), out.data_ptr(), y_dtype, _stream(dev)))
-    return out
+        w_s_enc.data_ptr(), y.data_ptr(), y_dtype, _stream(dev)))
+    _written(out)
+    return y
 
 
 def nvfp4_gated_matvec(act: int, x: torch.Tensor, gate_codes: torch.Tensor, gate_scales: torch.Tensor,
@@ -507,12 +519,13 @@ def nvfp4_gated_matvec(act: int, x: torch.Tensor, gate_codes: torch.Tensor, gate
     Fu, urows = _weights(up_codes, up_scales, up_s_enc, K, "up", dev)
     if Fu != F or urows != rows:
         raise ValueError("gate and up must agree in rows and in the kind of their tensor scales")
-    out = _output(out, (M, F), torch.bfloat16, dev)
+    h = _output(out, (M, F), torch.bfloat16, dev)
     _check("nvfp4_gated_matvec", lib().nvfp4_gated_matvec(
         FMT_B_ROWSCALED if rows else 0, act, M, F, K, x.data_ptr(), ldx, gate_codes.data_ptr(),
         gate_scales.data_ptr(), gate_s_enc.data_ptr(), up_codes.data_ptr(), up_scales.data_ptr(),
-        up_s_enc.data_ptr(), out.data_ptr(), _stream(dev)))
-    return out
+        up_s_enc.data_ptr(), h.data_ptr(), _stream(dev)))
+    _written(out)
+    return h
 
 
 # ---------------------------------------------------------------- the gated block's products
@@ -555,16 +568,17 @@ def blockscaled_gated_gemm(fmt: int, act: int, a_codes: torch.Tensor, a_scales: 
     if gate != up or gate[1] != K:
         raise ValueError("operands disagree: a [%d, %d], gate %s, up %s" % (M, K, list(gate), list(up)))
     F = gate[0]
-    h = _output(out, (M, F), torch.bfloat16, dev)
+    h, gu = _output(out, (M, F), torch.bfloat16, dev), None
     if save_gate_up:
-        gate_up = _output(gate_up, (M, 2 * F), torch.bfloat16, dev)
+        gu = _output(gate_up, (M, 2 * F), torch.bfloat16, dev)
     elif gate_up is not None:
         raise ValueError("gate_up is written with save_gate_up only")
     _check("blockscaled_gated_gemm", lib().blockscaled_gated_gemm(
         fmt, act, M, F, K, a_codes.data_ptr(), a_scales.data_ptr(), _ptr(a_s_enc), gate_codes.data_ptr(),
         gate_scales.data_ptr(), _ptr(gate_s_enc), up_codes.data_ptr(), up_scales.data_ptr(), _ptr(up_s_enc),
-        h.data_ptr(), _ptr(gate_up), _stream(dev)))
-    return (h, gate_up) if save_gate_up else h
+        h.data_ptr(), _ptr(gu), _stream(dev)))
+    _written(out, gate_up)
+    return (h, gu) if save_gate_up else h
 
 
 def blockscaled_gated_gemm_backward(fmt: int, act: int, dy_codes: torch.Tensor, dy_scales: torch.Tensor,
@@ -587,6 +601,7 @@ def blockscaled_gated_gemm_backward(fmt: int, act: int, dy_codes: torch.Tensor, 
     _check("blockscaled_gated_gemm_backward", lib().blockscaled_gated_gemm_backward(
         fmt, act, M, F, K, dy_codes.data_ptr(), dy_scales.data_ptr(), _ptr(dy_s_enc), w_codes.data_ptr(),
         w_scales.data_ptr(), _ptr(w_s_enc), gate_up.data_ptr(), d.data_ptr(), _stream(dev)))
+    _written(out)
     return d
 
 
@@ -640,7 +655,7 @@ class _GradList:
             if numels != self.numels or dtypes != self.dtypes:
                 i = next(i for i in range(len(out)) if numels[i] != self.numels[i] or dtypes[i] != self.dtypes[i])
                 raise ValueError("out[%d] must have its gradient's type and number of elements" % i)
-        self.n, self.device = len(grads), dev
+        self.n, self.device, self.written = len(grads), dev, grads if out is None else out
 
     @staticmethod
     def _arrays(tensors: list, name: str, dev):
@@ -682,6 +697,7 @@ def grad_clip(grads: Sequence[torch.Tensor], sumsq: torch.Tensor, max_norm: floa
         raise ValueError("sumsq must hold one value on %s" % (g.device,))
     norm = torch.empty(1, dtype=torch.float32, device=g.device)
     _check("grad_clip", lib().grad_clip(*g.args(), sumsq.data_ptr(), max_norm, norm.data_ptr(), _stream(g.device)))
+    torch.autograd.graph.increment_version(g.written)   # as _written
     return norm
 
 
@@ -695,6 +711,7 @@ def clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, out: Optional
     norm = torch.empty(1, dtype=torch.float32, device=g.device)
     _check("clip_grad_norm", lib().clip_grad_norm(*g.args(), max_norm, norm.data_ptr(), ws.data_ptr(),
                                                   _stream(g.device)))
+    torch.autograd.graph.increment_version(g.written)   # as _written
     return norm
 
 
@@ -789,9 +806,10 @@ def moe_gather(x: torch.Tensor, positions: torch.Tensor, source: torch.Tensor,
     T, H, ldx = _rows(x, torch.bfloat16, "x")
     dev = x.device
     k, R = _slots(positions, T, dev), _source(source, dev)
-    out = _output(out, (R, H), torch.bfloat16, dev)
-    _call("moe_gather", dev, T, k, H, x.data_ptr(), ldx, positions.data_ptr(), source.data_ptr(), R, out.data_ptr())
-    return out
+    xs = _output(out, (R, H), torch.bfloat16, dev)
+    _call("moe_gather", dev, T, k, H, x.data_ptr(), ldx, positions.data_ptr(), source.data_ptr(), R, xs.data_ptr())
+    _written(out)
+    return xs
 
 
 def moe_gather_nvfp4_rowscaled(x: torch.Tensor, positions: torch.Tensor, source: torch.Tensor) -> Dict[str, torch.Tensor]:
@@ -846,9 +864,10 @@ def moe_combine(y: torch.Tensor, positions: torch.Tensor, weights: Optional[torc
     k = _slots(positions, T, dev)
     _slot_weights(weights, positions)
     ot = _type(out_dtype, "out_dtype")
-    out = _output(out, (T, H), out_dtype, dev)
-    _call("moe_combine", dev, T, k, H, y.data_ptr(), yt, R, positions.data_ptr(), _ptr(weights), out.data_ptr(), ot)
-    return out
+    sums = _output(out, (T, H), out_dtype, dev)
+    _call("moe_combine", dev, T, k, H, y.data_ptr(), yt, R, positions.data_ptr(), _ptr(weights), sums.data_ptr(), ot)
+    _written(out)
+    return sums
 
 
 def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, positions: torch.Tensor, source: torch.Tensor,
@@ -908,7 +927,8 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, adapters: torch.Tensor, lora_a: t
     """Each token's low-rank adapter beside a projection's output y [M, N] (bf16 or float32; rows may be strided): y[m] +
     scales[a] (x[m] A_a^T) B_a^T with a = adapters[m] (int32; ids outside the adapters: none), x [M, K] bf16 (rows may be
     strided), lora_a [adapters, rank, K] and lora_b [adapters, N, rank] bf16, scales float32 or None for ones.
-    Written to y itself, or to ``out`` [M, N].  ``workspace``: lib().lora_workspace_bytes(M, rank) bytes; one is
+    Written to y itself, or to ``out`` [M, N]; like every call, without autograd's knowledge but for the tensor's version, so
+    that a y which a backward pass has saved is refused there.  ``workspace``: lib().lora_workspace_bytes(M, rank) bytes; one is
     allocated when none is given."""
     M, K, ldx = _rows(x, torch.bfloat16, "x")
     dev = x.device
@@ -926,6 +946,7 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, adapters: torch.Tensor, lora_a: t
     ws = _workspace(workspace, max(lib().lora_workspace_bytes(M, r), 0), dev)
     _call("lora_add", dev, M, N, K, r, n, x.data_ptr(), ldx, adapters.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(),
           _ptr(scales), y.data_ptr(), ldy, out.data_ptr(), ldo, yt, ws.data_ptr())
+    _written(out)
     return out
 
 
@@ -941,9 +962,10 @@ def nvfp4_lora_matvec(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Te
     N, rows = _weights(w_codes, w_scales, w_s_enc, K, "w", dev)
     r, n = _adapters(adapters, lora_a, lora_b, scales, M, N, K, dev)
     y_dtype = _type(out_dtype, "out_dtype")
-    out = _output(out, (M, N), out_dtype, dev)
+    y = _output(out, (M, N), out_dtype, dev)
     ws = _workspace(workspace, max(lib().nvfp4_lora_workspace_bytes(M, N, r, y_dtype), 0), dev)
     _call("nvfp4_lora_matvec", dev, FMT_B_ROWSCALED if rows else 0, M, N, K, x.data_ptr(), ldx, w_codes.data_ptr(),
           w_scales.data_ptr(), w_s_enc.data_ptr(), r, n, adapters.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(),
-          _ptr(scales), out.data_ptr(), y_dtype, ws.data_ptr())
-    return out
+          _ptr(scales), y.data_ptr(), y_dtype, ws.data_ptr())
+    _written(out)
+    return y
