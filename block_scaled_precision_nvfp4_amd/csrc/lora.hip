@@ -162,7 +162,7 @@ __device__ __forceinline__ void lora_store(const LoraArgs& a, int64_t m, int64_t
 // The up products of a tile of 16 tokens per wave by `chunks` times 64 columns, one after another.  The workgroup's waves
 // take neighbouring tiles, which mostly share an adapter: its 64 rows of B come through LDS, whole lines at a time,
 // for all of them, the next ones (and y's) asked for before the present ones are used.  t comes as the matrix
-// instruction's fragments, in three bf16 parts that add up to it exactly.  Column r16 of block b stands for column 4 r16 + b,
+// instruction's fragments, in three bf16 parts (lora_split).  Column r16 of block b stands for column 4 r16 + b,
 // so that a lane ends with 4 adjacent columns of each of 4 tokens (4 g + i) and 16 lanes read and write 128 (or 256)
 // adjacent bytes of y.
 constexpr int LORA_UP_WAVES = 4, LORA_COLS = 64;

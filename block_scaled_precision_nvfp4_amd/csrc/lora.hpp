@@ -26,8 +26,9 @@ struct LoraArgs {
 
 __host__ __device__ constexpr int lora_steps(int r) { return (r + 31) / 32; }
 
-// A value as three bf16 parts that add up to it exactly (8 bits of the significand each, cut, not rounded, so that a
-// large value does not become infinite).  An infinity or NaN goes into the first part alone.
+// A value as three bf16 parts that add up to it: 8 bits of the significand each, cut, not rounded, so that a large value
+// does not become infinite.  Exact from 2^-110 on; below, what lies under bf16's smallest value is cut off, less than 2^-133
+// (the matrix instruction takes subnormal parts as they are).  An infinity or NaN goes into the first part alone.
 __device__ __forceinline__ void lora_split(float v, uint16_t (&part)[3]) {
     const uint32_t u = __float_as_uint(v);
     const bool fin = (u & 0x7F800000u) != 0x7F800000u;

@@ -602,7 +602,8 @@ int moe_combine_backward(int64_t tokens, int64_t k, int64_t width, const void* d
  *              (smaller ones are padded with zeros).  scales float[num_adapters] (device), or NULL: 1.
  *   workspace  device scratch of lora_workspace_bytes(M, rank) or nvfp4_lora_workspace_bytes(M, N, rank, y_dtype) bytes,
  *              as for nvfp4_quantize.
- * Products of bf16 values are exact and added up in fp32; the result is rounded once, to y's type.  A NaN or an infinity
+ * Products of bf16 values are exact and added up in fp32; the result is rounded once, to y's type.  (Of more than 64
+ * tokens, a down product below 2^-110 loses what it has below 2^-133.)  A NaN or an infinity
  * in a token reaches that token's outputs only, one in an adapter the tokens that have it (where it may turn from an
  * infinity into a NaN).  Up to 64 tokens, adapters may be mixed at will; of more, tokens of one adapter should stand
  * together (moe_sort and moe_gather bring them so): every 16 tokens read each adapter that occurs among them.

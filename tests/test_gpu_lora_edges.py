@@ -1,4 +1,5 @@
-"""Adapters where the kernels of many tokens can go wrong: every shape of their launches with K of several pieces.
+"""Adapters where the kernels of many tokens can go wrong: every shape of their launches with K of several pieces, values
+that are not finite and values at the ends of fp32's range among mixed adapters.
 
 Tolerances as in test_gpu_lora."""
 import pytest
@@ -54,3 +55,64 @@ def test_matvec_in_whole_blocks_of_columns(M, N, K, r, L, dtype):
     intact()
     want = base + v
     assert_within(got, want, sum_error(K, S) + e + want.abs() * F32 + store_error(want, dtype), "y")
+
+
+@pytest.mark.parametrize("M,r", [(100, 24), (300, 64), (4100, 64)])
+def test_values_that_are_not_finite_among_many_tokens(M, r):
+    """Tiles of 16 tokens with four adapters each: a value spoils its token, or its adapter's tokens, and no bit of another."""
+    N, K, L = 72, 272, 4
+    x, ad, a, b, s = case(M, N, K, r, L, none=0.1)
+    ad[:5] = torch.tensor([0, 1, 2, 3, 1], dtype=torch.int32)
+    y, w = gauss(M, N, seed=8), weights(N, K, 4)
+    f = lambda: (bsq.lora_add(y, x, ad, a, b, s, out=torch.empty_like(y)).cpu(),   # noqa: E731
+                 bsq.nvfp4_lora_matvec(x, *w, ad, a, b, s).cpu())
+    clean = f()
+    assert all(torch.isfinite(t).all() for t in clean)
+    for value in (float("nan"), float("inf"), -float("inf")):
+        for m in (2, 31, M - 1):
+            ad_m = int(ad[m])
+            ad[m] = 2
+            want = f()
+            keep = x[m, 7].clone()
+            x[m, 7] = value   # a token
+            for got, ref in zip(f(), want):
+                assert not torch.isfinite(got[m]).any()
+                got[m] = ref[m]
+                assert torch.equal(got, ref)
+            x[m, 7] = keep
+            ad[m] = ad_m
+        mine = (ad == 1).cpu().nonzero().reshape(-1)
+        for t, at, cols in ((a, (1, 5, K - 1), slice(None)), (b, (1, 11, r - 1), 11)):   # a value of adapter 1
+            keep = t[at].clone()
+            t[at] = value
+            for got, want in zip(f(), clean):
+                assert not torch.isfinite(got[mine][:, cols]).any()
+                got[mine, cols] = want[mine, cols]
+                assert torch.equal(got, want)
+            t[at] = keep
+    s[3] = float("nan")
+    for got, want in zip(f(), clean):
+        mine = (ad == 3).cpu()
+        assert torch.isnan(got[mine]).all() and torch.equal(got[~mine], want[~mine])
+
+
+@pytest.mark.parametrize("M", [40, 100, 300])
+def test_large_and_small_down_products_side_by_side(M):
+    """Down products of up to 2^127, whose bf16 rounding would be infinite, beside some of 2^-97 and of 2^-115 in the same tiles.
+    Parts of a down product below 2^-133, bf16's smallest value, are cut off: r 2^-133 |b| a column more."""
+    N, K, r, L = 64, 64, 8, 3
+    x, a, b = gauss(M, K, seed=1), gauss(L, r, K, seed=2), gauss(L, N, r, seed=3)
+    ad = (torch.arange(M) * 7 % 5 % 4).to(torch.int32).to(DEV)   # 3: none
+    for i, (ex, ea, eb) in enumerate(((2.0 ** 60, 2.0 ** 62, 2.0 ** -100), (2.0 ** -50, 2.0 ** -50, 2.0 ** 90),
+                                      (2.0 ** -59, 2.0 ** -59, 2.0 ** 100))):
+        x[ad == i] *= ex
+        a[i] *= ea
+        b[i] *= eb
+    v, e = lora64(x, ad, a, b, None)
+    id_, on = ad.cpu().long(), (ad < 3).cpu()
+    cut = torch.zeros(M, N, dtype=torch.float64)
+    cut[on] = 2.0 ** -133 * b.cpu().double().abs().sum(2)[id_[on]]
+    y = torch.zeros((M, N), device=DEV)
+    got = bsq.lora_add(y, x, ad, a, b, out=torch.empty_like(y))
+    assert_within(got, v, e + cut + v.abs() * 2 * F32, "out")
+    assert (v[on].abs().amax(1) > 0).all() and float((x[ad == 0].cpu().double() @ a[0].cpu().double().t()).abs().max()) > 2.0 ** 126
