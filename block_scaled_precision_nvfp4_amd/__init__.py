@@ -850,7 +850,8 @@ def _slot_weights(weights: Optional[torch.Tensor], positions: torch.Tensor):
 def moe_combine(y: torch.Tensor, positions: torch.Tensor, weights: Optional[torch.Tensor] = None,
                 out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The experts' rows y [rows, H] (bf16 or float32) back to their tokens: out[t] = sum_j weights[t, j] y[positions[t, j]]
-    (fp32, rounded once) as [T, H] of ``out_dtype`` (bf16 or float32).  ``weights`` [T, k] float32, or None for ones."""
+    (fp32, rounded once) as [T, H] of ``out_dtype`` (bf16 or float32).  ``weights`` [T, k] float32, or None for ones.  Its
+    gradients: ``moe_combine_backward``, without weights ``moe_gather(dout, ...)``; both take dout in bf16."""
     if not isinstance(y, torch.Tensor):
         raise TypeError("y must be a tensor")
     yt = _type(y.dtype, "y")
@@ -928,7 +929,9 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, adapters: torch.Tensor, lora_a: t
     scales[a] (x[m] A_a^T) B_a^T with a = adapters[m] (int32; ids outside the adapters: none), x [M, K] bf16 (rows may be
     strided), lora_a [adapters, rank, K] and lora_b [adapters, N, rank] bf16, scales float32 or None for ones.
     Written to y itself, or to ``out`` [M, N]; like every call, without autograd's knowledge but for the tensor's version, so
-    that a y which a backward pass has saved is refused there.  ``workspace``: lib().lora_workspace_bytes(M, rank) bytes; one is
+    that a y which a backward pass has saved is refused there.  Its gradient towards x is the same call on dy [M, N],
+    ``lora_add(zeros [M, K], dy, adapters, B^T [adapters, rank, N], A^T [adapters, K, rank], scales)``, where N has to be a
+    multiple of 8 as K does here (zero columns fill dy and B^T up).  ``workspace``: lib().lora_workspace_bytes(M, rank) bytes; one is
     allocated when none is given."""
     M, K, ldx = _rows(x, torch.bfloat16, "x")
     dev = x.device

@@ -585,7 +585,7 @@ int moe_gather_mxfp8(int64_t tokens, int64_t k, int64_t width, const void* x, in
  *
  * moe_combine_backward -- its gradients: dy[positions[t][j]] = weights[t][j] * dout[t], zeros in rows without a source,
  * and dweights[t][j] = <dout[t], y[positions[t][j]]> in fp32, 0 for a dropped slot.
- *   dout [tokens][width] bf16; dy [rows][width] of y's type; dweights float[tokens][k].
+ *   dout [tokens][width] bf16, whatever out's type was; dy [rows][width] of y's type; dweights float[tokens][k].
  * Sizes as for moe_gather.
  */
 int moe_combine(int64_t tokens, int64_t k, int64_t width, const void* y, int y_dtype, int64_t rows,
@@ -608,7 +608,10 @@ int moe_combine_backward(int64_t tokens, int64_t k, int64_t width, const void* d
  * infinity into a NaN).  Up to 64 tokens, adapters may be mixed at will; of more, tokens of one adapter should stand
  * together (moe_sort and moe_gather bring them so): every 16 tokens read each adapter that occurs among them.
  *
- * lora_add -- beside any projection, whose output y is given.
+ * lora_add -- beside any projection, whose output y is given.  The gradient towards x is the same call on dy with the
+ * adapters' matrices in each other's place, transposed: dx = 0 + s_a (dy[m] B_a) A_a, lora_a being B^T [num_adapters][rank][N]
+ * and lora_b A^T [num_adapters][K][rank]; N is then along the products, a multiple of 8 as K is here (columns of zeros fill dy
+ * and B^T up).  Gradients towards A, B and the scales are not part of the library.
  *   y, out     bf16 or fp32 (y_dtype), rows ldy and ldo elements apart (a projection's slice of a wider output); out
  *              is y itself with ldo == ldy (in place), or overlaps no other argument.  Aligned to their elements.
  *   K % 8 == 0, K < 2^24; M <= 2^20; N any with ceil(M / 64) ceil(N / 64) < 2^24.

@@ -1,5 +1,5 @@
 """Adapters where the kernels of many tokens can go wrong: every shape of their launches with K of several pieces, values
-that are not finite and values at the ends of fp32's range among mixed adapters.
+that are not finite and values at the ends of fp32's range among mixed adapters, and the gradient towards the tokens.
 
 Tolerances as in test_gpu_lora."""
 import pytest
@@ -116,3 +116,42 @@ def test_large_and_small_down_products_side_by_side(M):
     got = bsq.lora_add(y, x, ad, a, b, out=torch.empty_like(y))
     assert_within(got, v, e + cut + v.abs() * 2 * F32, "out")
     assert (v[on].abs().amax(1) > 0).all() and float((x[ad == 0].cpu().double() @ a[0].cpu().double().t()).abs().max()) > 2.0 ** 126
+
+
+def towards_tokens(dy, ad, a, b, s):
+    """The gradient of lora_add with respect to x, fp32: lora_add with A^T and B^T in each other's place, K and N as well; N is
+    then along the products, so dy and B get columns of zeros up to a multiple of 8."""
+    N = dy.shape[1]
+    pad = -N % 8
+    dy = torch.nn.functional.pad(dy, (0, pad))
+    bt = torch.nn.functional.pad(b.transpose(1, 2), (0, pad)).contiguous()
+    dx = torch.zeros((dy.shape[0], a.shape[2]), device=DEV)
+    return bsq.lora_add(dx, dy, ad, bt, a.transpose(1, 2).contiguous(), s)
+
+
+@pytest.mark.parametrize("M,N,K,r,L", [(1, 64, 64, 8, 2), (5, 100, 136, 16, 3), (40, 257, 72, 24, 4), (100, 130, 520, 64, 5),
+                                       (300, 64, 200, 40, 3)])
+def test_gradient_towards_the_tokens(M, N, K, r, L):
+    note("lora gradient %d %d %d %d %d" % (M, N, K, r, L))
+    x, ad, a, b, s = case(M, N, K, r, L, seed=M + N)
+    dy = gauss(M, N, seed=5)
+    dx = towards_tokens(dy, ad, a, b, s).cpu().double()
+    want, e = lora64(dy, ad, b.transpose(1, 2), a.transpose(1, 2), s)   # (dy B) A
+    assert_within(dx, want, e + want.abs() * F32, "dx")
+    # <f(x1) - f(x2), dy> = <x1 - x2, dx>, f being linear in x: exact but for f's errors on either side, each weighted
+    # by |dy|, and dx's, weighted by |x1 - x2|.  f starts from zeros, in fp32: one rounding more of the output.
+    x1, x2 = (x + gauss(M, K, seed=6)), (x - gauss(M, K, seed=7))
+    zeros = torch.zeros((M, N), device=DEV)
+    f = lambda t: bsq.lora_add(zeros, t, ad, a, b, s, out=torch.empty_like(zeros)).cpu().double()   # noqa: E731
+    (v1, e1), (v2, e2) = (lora64(t, ad, a, b, s) for t in (x1, x2))
+    step, d = x1.cpu().double() - x2.cpu().double(), dy.cpu().double()
+    tol = ((e1 + e2 + (v1.abs() + v2.abs()) * F32) * d.abs()).sum() + (step.abs() * (e + want.abs() * F32)).sum()
+    assert abs(float(((f(x1) - f(x2)) * d).sum() - (step * dx).sum())) <= float(tol) * (1 + 2.0 ** -20)
+
+
+def test_the_gradient_needs_whole_pieces_of_the_columns():
+    x, ad, a, b, s = case(4, 100, 64, 16, 2)
+    dx, dy = torch.zeros((4, 64), device=DEV), gauss(4, 100, seed=1)
+    with pytest.raises(bsq.BsqError):   # 100 columns are not a multiple of 8
+        bsq.lora_add(dx, dy, ad, b.transpose(1, 2).contiguous(), a.transpose(1, 2).contiguous(), s)
+    assert not dx.any()
