@@ -828,7 +828,8 @@ def moe_gather_nvfp4_rowscaled(x: torch.Tensor, positions: torch.Tensor, source:
 
 def moe_gather_mxfp8(x: torch.Tensor, positions: torch.Tensor, source: torch.Tensor) -> Dict[str, torch.Tensor]:
     """``mxfp8_quantize(moe_gather(x, positions, source))`` without the copy in between: ``row_codes`` [rows, H],
-    ``row_scales`` [rows, H/32] (uint8)."""
+    ``row_scales`` [rows, H/32] (uint8); equal for finite values.  A value that is not finite becomes the NaN code under
+    the scale byte 247, where the cast's codes of its block depend on the blocks beside it."""
     T, H, ldx = _rows(x, torch.bfloat16, "x")
     dev = x.device
     k, R = _slots(positions, T, dev), _source(source, dev)
