@@ -1,12 +1,12 @@
-"""Experts' operators where they can go wrong: row-scaled NVFP4 gathers at the widths of every kernel, and MXFP8 blocks at the
-bottom of the scales' range and of negative zeros."""
+"""Experts' operators where they can go wrong: row-scaled NVFP4 gathers at the widths of every kernel, MXFP8 blocks at the bottom
+of the scales' range and of negative zeros, and outputs of all operators in guarded buffers through the C entry points."""
 import numpy as np
 import pytest
 import torch
 
 import block_scaled_precision_nvfp4_amd as bsq
 from tests.gpu_common import note
-from tests.test_gpu_moe import DEV, gauss, order_of, rows_of
+from tests.test_gpu_moe import DEV, gauss, ids, order_of, rows_of
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,71 @@ def test_mxfp8_gathers_of_tiny_blocks(T, k, E, H):
     want = oracle.mxfp8_quantize(got.cpu()[:400], direction=oracle.ROW)
     for n in ("row_codes", "row_scales"):
         assert np.array_equal(q[n].cpu().numpy()[:400], want[n]), n
+
+
+def guard(shape, dtype):
+    """A 16-byte aligned tensor inside a marked buffer, and a check that nothing around it changed."""
+    n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+    pad = max(4096, 272 * int(shape[-1]) * 4) // 16 * 16
+    buf = torch.full((pad + n + pad,), 0xA5, dtype=torch.uint8, device=DEV)
+
+    def intact():
+        assert (buf[:pad] == 0xA5).all(), "written before an output"
+        assert (buf[pad + n:] == 0xA5).all(), "written after an output"
+    return buf[pad:pad + n].view(dtype).view(shape), intact
+
+
+def call(fn, *args):
+    at = [t.data_ptr() if isinstance(t, torch.Tensor) else t for t in args]
+    assert getattr(bsq.lib(), fn)(*at, torch.cuda.current_stream().cuda_stream) == 0, bsq.lib().bsq_last_error()
+
+
+# rows that end inside a wave's or a lane's part, few and many tokens, each kernel of the gathers, rows without a slot at the end
+@pytest.mark.parametrize("T,k,E,H", [(1, 1, 1, 32), (3, 2, 4, 96), (37, 3, 8, 1056), (100, 2, 5, 4128), (2050, 2, 6, 608), (2050, 2, 6, 2080),
+                                     (9, 4, 8, 8224)])
+def test_nothing_is_written_outside_the_outputs(T, k, E, H):
+    note("guarded routed outputs %d %d %d %d" % (T, k, E, H))
+    e = ids(T, k, E, T, drop=0.1).to(DEV)
+    n, L = T * k, bsq.lib()
+    R = L.moe_sort_rows(n, E, 16)
+    ws = torch.empty(max(L.moe_sort_workspace_bytes(n, E), 16), dtype=torch.uint8, device=DEV)
+    (offs, a), (p, b), (s, c) = guard((E + 1,), torch.int64), guard((T, k), torch.int32), guard((R,), torch.int32)
+    call("moe_sort", e, 8, n, E, 16, R, offs, p, s, ws)
+    checks, want = [a, b, c], bsq.moe_sort(e, E, 16)
+    assert torch.equal(offs, want["offsets"]) and torch.equal(p, want["positions"]) and torch.equal(s, want["source"])
+    x, w = gauss(T, H, seed=1).to(DEV), gauss(T, k, seed=2, dtype=torch.float32).to(DEV)
+    (codes, a), (scales, b), (s_enc, c) = guard((R, H // 2), torch.uint8), guard((R, H // 16), torch.uint8), guard((R,), torch.float32)
+    call("moe_gather_nvfp4_rowscaled", T, k, H, x, H, p, s, R, codes, scales, s_enc)
+    checks += [a, b, c]
+    q = bsq.moe_gather_nvfp4_rowscaled(x, p, s)
+    assert torch.equal(codes, q["codes"]) and torch.equal(scales, q["scales"]) and torch.equal(s_enc, q["s_enc"])
+    (codes, a), (scales, b) = guard((R, H), torch.uint8), guard((R, H // 32), torch.uint8)
+    call("moe_gather_mxfp8", T, k, H, x, H, p, s, R, codes, scales)
+    checks += [a, b]
+    q = bsq.moe_gather_mxfp8(x, p, s)
+    assert torch.equal(codes, q["row_codes"]) and torch.equal(scales, q["row_scales"])
+    for code, dtype in ((bsq.OUT_BF16, torch.bfloat16), (bsq.OUT_F32, torch.float32)):
+        y = gauss(R, H, seed=3, dtype=dtype).to(DEV)
+        (dy, a), (dw, b) = guard((R, H), dtype), guard((T, k), torch.float32)
+        call("moe_combine_backward", T, k, H, x, y, code, R, p, s, w, dy, dw)
+        checks += [a, b]
+        want_dy, want_dw = bsq.moe_combine_backward(x, y, p, s, w)
+        assert torch.equal(dy, want_dy) and torch.equal(dw, want_dw)
+    for intact in checks:
+        intact()
+
+
+def test_large_outputs_stay_inside_their_buffers():
+    """Outputs that are stored past the caches."""
+    T, k, E, H = 33003, 2, 5, 2048
+    p, s = order_of(T, k, E, 32, 1)
+    x, w = gauss(T, H, seed=1).to(DEV), gauss(T, k, seed=2, dtype=torch.float32).to(DEV)
+    R = s.numel()
+    for code, dtype in ((bsq.OUT_BF16, torch.bfloat16), (bsq.OUT_F32, torch.float32)):
+        y = bsq.moe_gather(x, p, s).to(dtype)
+        (dy, a), (dw, b) = guard((R, H), dtype), guard((T, k), torch.float32)
+        call("moe_combine_backward", T, k, H, x, y, code, R, p, s, w, dy, dw)
+        a()
+        b()
+        want_dy, want_dw = bsq.moe_combine_backward(x, y, p, s, w)
+        assert torch.equal(dy, want_dy) and torch.equal(dw, want_dw)
