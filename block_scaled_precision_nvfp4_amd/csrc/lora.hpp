@@ -43,6 +43,14 @@ __device__ __forceinline__ void lora_split(float v, uint16_t (&part)[3]) {
 
 // Few tokens: a wave takes a token's products with RQ rows of its adapter's A, U pieces of 512 elements at a time, all
 // their loads in flight at once: t[m][q] as fp32.  Unit `unit` of lora_few_units, 64 lanes.
+//
+// us of a whole call, 4096 x 4096, its tokens taken so and in tiles (lora_down_kernel, lora_up_kernel), rank 16 and rank 64:
+//   64 tokens of one adapter   6.7 and 11.4,  11.1 and 11.6     64 of 64, mixed     9.6 and 46,  19 and 58
+//   128 of one                 7.8 and 11.8,  14.0 and 12.2     128 of 128, mixed    12 and 47,  31 and 66
+//   128 of 8 in runs           7.8 and 13.1,  14.9 and 15.5     128 of 8, mixed     7.9 and 16,  15 and 20
+//   256 of one                12.1 and 11.9,  22.2 and 12.3     256 of 256, mixed    21 and 49,  54 and 82
+// So tiles pay from 64 tokens of one adapter on with large ranks, and from 128 to 256 with small ones; of mixed adapters
+// later than 256.  The limit is at the first of these and looks at neither.
 constexpr int LORA_FEW = 64;   // tokens at most
 
 __host__ __device__ inline int64_t lora_few_units(int64_t M, int r, int rq) { return M * ((r + rq - 1) / rq); }

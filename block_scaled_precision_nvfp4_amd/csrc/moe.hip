@@ -195,7 +195,9 @@ __global__ __launch_bounds__(64 * SORT_WAVES) void moe_place_kernel(SortArgs a) 
 // The launch's shape: one workgroup up to 4096 slots, of as many waves as have slots; else a count first, and
 // several workgroups, each wave with 64 slots or, where that would be over 128 workgroups, more.  us in a graph, one
 // workgroup and several, 8 / 128 experts: 2048 slots 6.1 / 7.7 and 8.2 / 9.3, 4096 7.5 / 9.8 and 8.2 / 9.1 (a
-// second launch costs the host 2), 16384 16.2 / 22.1 and 8.4 / 9.6; with 128 slots a wave 9.5 / 11.1.  A few slots of
+// second launch costs the host 2), 16384 16.2 / 22.1 and 8.4 / 9.6; with 128 slots a wave 9.5 / 11.1.  Of 256 / 1000
+// experts 2048 slots take 8.5 / 16.2 and 9.7 / 12.8, 4096 10.8 / 19.7 and 9.6 / 11.1: there several workgroups would pay
+// earlier, and the limit does not look at the experts.  A few slots of
 // many experts take a wave for 16 experts too, which share their counts: 4 x 5 of 63, padded to 32, 7.0 and 5.1.
 constexpr int SORT_ONE = 4096, SORT_MINE = 64;
 
