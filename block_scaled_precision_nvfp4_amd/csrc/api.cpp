@@ -764,7 +764,7 @@ int moe_gather_nvfp4_rowscaled(int64_t tokens, int64_t k, int64_t width, const v
     static const char* fn = "moe_gather_nvfp4_rowscaled";
     const int st = gather_check(fn, tokens, k, width, 16, x, ldx, positions, source, rows, codes, scales);
     if (st) return st;
-    if (rows == 0 || width == 0) return ok();
+    if (rows == 0) return ok();
     if (!s_enc_rows) return fail(BSQ_ERR_NULL, "%s: s_enc_rows is NULL", fn);
     if (unaligned(s_enc_rows, 4)) return fail(BSQ_ERR_ALIGN, "%s: s_enc_rows is not aligned", fn);
     return launched(bsq::launch_moe_gather_nvfp4(x, ldx, tokens, k, width, positions, source, rows, codes, scales,

@@ -545,11 +545,21 @@ __global__ __launch_bounds__(MOE_THREADS) void moe_gather_nvfp4_kernel(GatherArg
     }
 }
 
+// Rows of width 0 have a scale all the same, that of a row without a value above 0.
+__global__ __launch_bounds__(MOE_THREADS) void moe_gather_scales_kernel(float* s_enc, int64_t rows) {
+    const int64_t r = (int64_t)blockIdx.x * MOE_THREADS + threadIdx.x;
+    if (r < rows) s_enc[r] = nvfp4_tensor_scale(0.0f);
+}
+
 int launch_moe_gather_nvfp4(const void* x, int64_t ldx, int64_t T, int64_t k, int64_t H, const int32_t* positions,
                             const int32_t* source, int64_t rows, uint8_t* codes, uint8_t* scales, float* s_enc,
                             void* hip_stream) {
     if (rows == 0) return 0;
     hipStream_t s = (hipStream_t)hip_stream;
+    if (H == 0) {
+        hipLaunchKernelGGL(moe_gather_scales_kernel, dim3((unsigned)((rows + MOE_THREADS - 1) / MOE_THREADS)), dim3(MOE_THREADS), 0, s, s_enc, rows);
+        return (int)hipGetLastError();
+    }
     // a wave a token where that leaves every CU eight of them, else a workgroup
     const bool wave = T >= 2048 && H <= 4096;
     const GatherArgs a{(const uint16_t*)x, ldx, H, {positions, source, T, (int)k, rows},

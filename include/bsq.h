@@ -563,7 +563,7 @@ int moe_sort(const void* experts, int id_bytes, int64_t slots, int64_t num_exper
  *   tokens <= 2^23, k <= 64, tokens * k <= 2^25, tokens * ceil(width / 512) <= 2^25.
  * moe_gather_nvfp4_rowscaled -- nvfp4_quantize_rowscaled (BSQ_RNE, no transform) of that out, bit for bit, without the
  * copy in between: a token is quantized once and its codes written to its k rows.  width % 16 == 0.
- *   codes [rows][width/2], scales [rows][width/16], s_enc_rows float[rows] (device).
+ *   codes [rows][width/2], scales [rows][width/16], s_enc_rows float[rows] (device), written for width 0 too.
  * moe_gather_mxfp8 -- likewise mxfp8_quantize with BSQ_ROW.  width % 32 == 0.  A value that is not finite becomes the NaN
  * code, under the scale byte 247 (the cast's codes of such a block depend on its neighbours).
  *   row_codes [rows][width], row_scales [rows][width/32] (device).

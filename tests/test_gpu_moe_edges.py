@@ -31,6 +31,29 @@ def test_nvfp4_gathers_of_many_wide_tokens(T, H):
         assert torch.equal(q[n], ref[n]), n
 
 
+@pytest.mark.parametrize("T", [0, 3, 3000])
+def test_nvfp4_gathers_of_width_zero(T):
+    """Rows without elements have a scale all the same, the cast's, by which a product along them divides."""
+    note("gather nvfp4 width 0, %d tokens" % T)
+    p, s = order_of(T, 2, 4, 32, 5) if T else order_of(0, 2, 4, 1, 5)
+    if T == 0:
+        s = torch.full((5,), -1, dtype=torch.int32, device=DEV)   # rows of padding only
+    x, R = torch.zeros((T, 0), dtype=torch.bfloat16, device=DEV), s.numel()
+    ref = bsq.nvfp4_quantize_rowscaled(bsq.moe_gather(x, p, s))
+    assert (ref["s_enc"] == 1).all()
+    s_enc, intact = guard((R,), torch.float32)
+    s_enc.fill_(float("nan"))
+    call("moe_gather_nvfp4_rowscaled", T, 2, 0, None, 0, p, s, R, None, None, s_enc)
+    intact()
+    assert torch.equal(s_enc, ref["s_enc"])
+    q = bsq.moe_gather_nvfp4_rowscaled(x, p, s)
+    assert all(torch.equal(q[n], ref[n]) for n in ("codes", "scales", "s_enc"))
+    b = bsq.nvfp4_quantize(torch.zeros((16, 0), dtype=torch.bfloat16, device=DEV))
+    y = bsq.blockscaled_gemm(bsq.FMT_NVFP4 | bsq.FMT_A_ROWSCALED, q["codes"], q["scales"], q["s_enc"], b["row_codes"],
+                             b["row_scales"], b["s_enc"][:1])
+    assert y.shape == (R, 16) and not y.any()
+
+
 def tiny_blocks(T, H, seed):
     """Ordinary blocks of 32, and among them blocks of 2^-112 (the least scale byte above 0 is that of 2^-118) down to bf16's
     smallest subnormals, blocks of negative zeros, of zeros of both signs, and of one value among negative zeros."""

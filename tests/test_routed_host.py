@@ -172,3 +172,11 @@ def test_binding_wants_device_tensors():
         bsq.lora_add(bf, bf, src, bf, bf)
     with pytest.raises(TypeError):
         bsq.nvfp4_lora_matvec(bf, bf, bf, f32, src, bf, bf)
+
+
+def test_a_gather_of_width_zero_still_writes_the_rows_scales(L):
+    two = dict(GATHER, scales=None, x=None, source=None, out=None, H=0, ldx=0)
+    assert call(L, "moe_gather_mxfp8", two, {}) == 0
+    assert call(L, "moe_gather_nvfp4_rowscaled", dict(two, s_enc=None), {}) == 1
+    assert call(L, "moe_gather_nvfp4_rowscaled", dict(two, s_enc=FAKE + 2), {}) == 6
+    assert call(L, "moe_gather_nvfp4_rowscaled", dict(two, s_enc=None), dict(rows=0)) == 0
