@@ -49,8 +49,9 @@ __device__ __forceinline__ void lora_split(float v, uint16_t (&part)[3]) {
 //   128 of one                 7.8 and 11.8,  14.0 and 12.2     128 of 128, mixed    12 and 47,  31 and 66
 //   128 of 8 in runs           7.8 and 13.1,  14.9 and 15.5     128 of 8, mixed     7.9 and 16,  15 and 20
 //   256 of one                12.1 and 11.9,  22.2 and 12.3     256 of 256, mixed    21 and 49,  54 and 82
-// So tiles pay from 64 tokens of one adapter on with large ranks, and from 128 to 256 with small ones; of mixed adapters
-// later than 256.  The limit is at the first of these and looks at neither.
+//   256 of 8, mixed             12 and 16,    25 and 25     96 of one          7.3 and 11.7,  12.8 and 12.1
+// So of one adapter tiles pay from between 64 and 96 tokens on with rank 64, from some 256 with rank 16; of mixed ones from 256
+// or later.  The limit is below the first of these and looks at neither ranks nor adapters.
 constexpr int LORA_FEW = 64;   // tokens at most
 
 __host__ __device__ inline int64_t lora_few_units(int64_t M, int r, int rq) { return M * ((r + rq - 1) / rq); }

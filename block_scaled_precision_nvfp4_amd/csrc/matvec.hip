@@ -507,9 +507,9 @@ static int launch_tokens(MvArgs a, hipStream_t s) {
         mv_downs(a, a.wr * parts, mb);
         const int64_t own = (blocks + a.wr - 1) / a.wr * mb;
         auto rounds = [](int64_t groups) { return (groups + MV_CUS - 1) / MV_CUS; };
-        // From 5 tokens on, in tiles of 16 or more, a workgroup has a CU to itself, and down products that begin another round of them wait, or
-        // make weights wait, for a whole one: they go first, in a launch of their own.  Rank 16, us together and
-        // so: 16 x 4096 x 14336 37.8 and 30.2, 16 x 8192 x 4096 21.8 and 19.1; tiles of 64 tokens, 64 x 14336 x 4096 of
+        // From 5 tokens on, in tiles of 16 or more, a workgroup has a CU to itself, and down products that begin another
+        // round of them wait, or make weights wait, for a whole one: they go first, in a launch of their own.  Rank 16, us
+        // together and so: 16 x 4096 x 14336 37.8 and 30.2, 16 x 8192 x 4096 21.8 and 19.1; tiles of 64 tokens, 64 x 14336 x 4096 of
         // rank 64, 43.7 and 45.0.  Past four rounds one more is no longer than that launch.
         if (T >= 16 && T < 64 && rounds(own) < 4 && rounds(own + a.downs * mb) > rounds(own)) {
             const int e = launch_lora_down_few(a.lora, s);
